@@ -341,8 +341,7 @@ l3_status l3_orthogonalize(const void *G, int64_t batch, int64_t rows, int64_t c
  * with X = l3_orthogonalize of U.
  *
  *   W   [batch x rows x cols] dtype (L3_BF16 weights are rounded once, to
- *       nearest; their X, from products on fewer parts, is off by 1e-3, up to
- *       7e-3 where few or equal singular values let the roundings add up)
+ *       nearest)
  *   M   fp32, the momentum (zeros before the first step)
  *   G   fp32, the gradient, as l3_backward writes dW_up and dW_mix
  *   scale  sqrt(max(1, rows / cols)) is usual

@@ -133,13 +133,6 @@ struct Products<1, 1> {
   __host__ __device__ static constexpr int frees(int) { return 0; }
 };
 template <>
-struct Products<1, 2> {  // hi lo, hi hi
-  static constexpr int N = 2;
-  __host__ __device__ static constexpr int a(int) { return 0; }
-  __host__ __device__ static constexpr int b(int i) { return i == 0; }
-  __host__ __device__ static constexpr int frees(int i) { return i == 0; }
-};
-template <>
 struct Products<2, 1> {  // lo hi, hi hi
   static constexpr int N = 2;
   __host__ __device__ static constexpr int a(int i) { return i == 0; }

@@ -18,13 +18,10 @@
 // thousand times the rest, the pairs 6e-6. fp16's narrow range is no limit:
 // |X| <= 1.3, |A| <= 1.6 and |B| <= 2.9 elementwise once the norm is divided
 // out, so each is stored times a fixed power of two near the top of the range.
-// Where the update goes into a bf16 W, A and B are held in one fp16 part and only
-// X in two: A's and B's rounding enters each step afresh and is not grown by the
-// later ones as X's is. The update is 1e-3 off for noise, 7e-3 where few or equal
-// singular values let the roundings add up (4 x 1573; X in one part too: 3e-2),
-// against half a step of W, 4e-3 of all of it. 15 products instead of 21: 2048 x
-// 4096 takes 543 us, two parts 704. O itself in bf16 keeps two parts, whose error
-// stays far below its rounding in every case.
+// A bf16 result takes the same pairs: with A and B in one part (15 products instead
+// of 21) an update is 1e-3 off for noise and 7e-3 where few or equal singular values
+// let the roundings add up, which a W that is large beside it hides, but not one
+// that starts at zero.
 // Where eps is not small beside |U|, X starts below one and V = X 2^e, of norm
 // in (1/2, 1], is held in its place: e falls by two a step (V grows by at most
 // a < 4) until X itself is, and the polynomial's coefficients take the powers
@@ -225,14 +222,13 @@ __device__ __forceinline__ int exp_at(const int *exps, int b, int done) {
 // The hi (and lo) boxes of a stack's matrices (planes of batch x mp rows) as an
 // epilogue warp's operand. A tile's first columns are asked for while its
 // products still run, the next ones when the boxes have been copied out.
-template <int PARTS>
 struct PairIn {
   CUtensorMap map;
   int mp, batch_rows;  // rows of a matrix and of a plane
 
   __device__ __forceinline__ void fetch(pg::WarpBoxes &box, int b, int m_warp, int col) const {
     box.written();  // what the boxes held is done with
-    if (box.lane == 0) box.load<PARTS>(&map, col, b * mp + m_warp, batch_rows);
+    if (box.lane == 0) box.load<2>(&map, col, b * mp + m_warp, batch_rows);
   }
 };
 
@@ -252,24 +248,23 @@ __device__ __forceinline__ void turn_block(pg::WarpBoxes &box, float (&v)[32]) {
 }
 
 // eight elements of a warp's row from its boxes
-template <int PARTS>
 __device__ __forceinline__ void unpack(const pg::WarpBoxes &box, int j, float (&f)[8]) {
-  unpack_pair(*box.piece(0, j), PARTS == 2 ? *box.piece(1, j) : make_uint4(0, 0, 0, 0), f);
+  unpack_pair(*box.piece(0, j), *box.piece(1, j), f);
 }
 
 // A = X X^T (POLY = false) or B = a I + b A + c A A (POLY = true), both symmetric:
 // the blocks right of the diagonal one are not written
-template <int TN, bool POLY, int PARTS>
+template <int TN, bool POLY>
 struct EpiSym {
-  __half *out;  // PARTS planes of batch x mp x mp
+  __half *out;  // two planes of batch x mp x mp
   int64_t plane;
-  PairIn<PARTS> a;  // POLY: A
+  PairIn a;  // POLY: A
   int mp;
   const int *exps;
   int done;
 
   // A in (POLY), the result out
-  static constexpr int BOX_BYTES = PARTS * pg::BOX;
+  static constexpr int BOX_BYTES = 2 * pg::BOX;
   static constexpr bool LOADS = POLY;
   static constexpr int WARPS = 16;
   static constexpr bool SUMS = true;
@@ -298,7 +293,7 @@ struct EpiSym {
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       float f[8];
-      if (POLY) unpack<PARTS>(box, j, f);
+      if (POLY) unpack(box, j, f);
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
         f[e] = POLY ? fmaf(v[j * 8 + e], s.cc, s.cb * f[e]) : v[j * 8 + e] * exp2f(SA - 2 * SX);
@@ -307,12 +302,12 @@ struct EpiSym {
       uint4 hi, lo;
       pack_pair(f, hi, lo);
       *box.piece(0, j) = hi;
-      if (PARTS == 2) *box.piece(1, j) = lo;
+      *box.piece(1, j) = lo;
     }
     __syncwarp();
     __half *to = s.o + (int64_t)s.m_warp * mp + col;
     box.copy_out(0, to, mp);
-    if (PARTS == 2) box.copy_out(1, to + plane, mp);
+    box.copy_out(1, to + plane, mp);
   }
   __device__ __forceinline__ void end(State &) const {}
 };
@@ -357,7 +352,7 @@ struct EpiShare {
 // The shares of A (POLY = false) or A A (POLY = true) added up in their order,
 // and from the sum A or B as hi + lo planes: a 64 x 64 block in or left of the
 // 256-wide diagonal block per thread block. Memory-bound.
-template <bool POLY, int PARTS>
+template <bool POLY>
 __global__ void __launch_bounds__(256) k_sym_join(const float *share, int shares, int64_t batch,
                                                   int mp, const __half *a, const int *exps,
                                                   int done, __half *out) {
@@ -382,8 +377,7 @@ __global__ void __launch_bounds__(256) k_sym_join(const float *share, int shares
     __half2 hi[2], lo[2];
     if (POLY) {
       *reinterpret_cast<uint2 *>(hi) = *reinterpret_cast<const uint2 *>(a + at);
-      *reinterpret_cast<uint2 *>(lo) =
-          PARTS == 2 ? *reinterpret_cast<const uint2 *>(a + plane + at) : make_uint2(0, 0);
+      *reinterpret_cast<uint2 *>(lo) = *reinterpret_cast<const uint2 *>(a + plane + at);
     }
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
@@ -400,7 +394,7 @@ __global__ void __launch_bounds__(256) k_sym_join(const float *share, int shares
       split2(f[2 * h], f[2 * h + 1], hi[h], lo[h]);
     }
     *reinterpret_cast<uint2 *>(out + at) = *reinterpret_cast<uint2 *>(hi);
-    if (PARTS == 2) *reinterpret_cast<uint2 *>(out + plane + at) = *reinterpret_cast<uint2 *>(lo);
+    *reinterpret_cast<uint2 *>(out + plane + at) = *reinterpret_cast<uint2 *>(lo);
   }
 }
 
@@ -536,7 +530,7 @@ struct Chain {
   __half *x[2], *a, *bm;
   const int *exps;
   int64_t xr;  // rows of one plane
-  bool fp32, fine;  // the result's type; A and B in two parts
+  bool fp32;   // the result's type
   CUtensorMap x_m[2], x_n[2][2], x_k[2];  // X as M (128 rows), as N, as k rows
   CUtensorMap a_s, a_box, b_s;  // A and B as symmetric operands
 
@@ -577,32 +571,30 @@ struct Chain {
     return P;
   }
 
-  template <int TN, bool POLY, int PARTS>
+  template <int TN, bool POLY>
   l3_status sym_product(int cur, int done) {
     pg::Args P = args(TN, true);
     P.nkb = (int)((POLY ? L.mp : L.np) / pg::BK);
-    EpiSym<TN, POLY, PARTS> e{POLY ? bm : a, xr * L.mp, {a_box, (int)L.mp, (int)xr}, (int)L.mp, exps, done};
+    EpiSym<TN, POLY> e{POLY ? bm : a, xr * L.mp, {a_box, (int)L.mp, (int)xr}, (int)L.mp, exps, done};
     const CUtensorMap &mA = POLY ? a_s : x_m[cur], &mB = POLY ? a_s : x_n[cur][TN / 256];
     const int shares = POLY ? L.poly.splits : L.gram.splits;
     LaunchTimer t(POLY ? "muon_poly" : "muon_gram", s);
     constexpr pg::Major MAJOR = POLY ? pg::SYMMETRIC : pg::K_MAJOR;
-    constexpr int P_IN = POLY ? PARTS : 2;  // X is always in two
-    if (shares == 1) return pg::launch<TN, P_IN, P_IN, MAJOR, MAJOR>(mA, mB, P, e, device, s);
+    if (shares == 1) return pg::launch<TN, 2, 2, MAJOR, MAJOR>(mA, mB, P, e, device, s);
     P.splits = shares;
     P.batch *= shares;
     const EpiShare<TN> es{reinterpret_cast<float *>(ws + L.share), (int)L.mp};
-    const l3_status st = pg::launch<TN, P_IN, P_IN, MAJOR, MAJOR>(mA, mB, P, es, device, s);
+    const l3_status st = pg::launch<TN, 2, 2, MAJOR, MAJOR>(mA, mB, P, es, device, s);
     if (st != L3_OK) return st;
     const unsigned blocks = (unsigned)(L.mp / 64);
-    return pg::launch_link(k_sym_join<POLY, PARTS>, dim3(blocks, blocks, (unsigned)L.batch),
+    return pg::launch_link(k_sym_join<POLY>, dim3(blocks, blocks, (unsigned)L.batch),
                            dim3(256), s, true, es.out, shares, L.batch, (int)L.mp, a, exps, done,
                            POLY ? bm : a);
   }
   template <bool POLY>
   l3_status sym_product(int cur, int done) {
     const bool wide = (POLY ? L.poly : L.gram).tn == 256;
-    return fine ? wide ? sym_product<256, POLY, 2>(cur, done) : sym_product<128, POLY, 2>(cur, done)
-                    : wide ? sym_product<256, POLY, 1>(cur, done) : sym_product<128, POLY, 1>(cur, done);
+    return wide ? sym_product<256, POLY>(cur, done) : sym_product<128, POLY>(cur, done);
   }
   template <int TN, class E>
   l3_status step(int cur, E &e, int done) {
@@ -611,8 +603,7 @@ struct Chain {
     e.exps = exps;
     e.done = done;
     LaunchTimer t("muon_step", s);
-    return fine ? pg::launch<TN, 2, 2, pg::SYMMETRIC, pg::MN_MAJOR>(b_s, x_k[cur], P, e, device, s)
-                    : pg::launch<TN, 1, 2, pg::SYMMETRIC, pg::MN_MAJOR>(b_s, x_k[cur], P, e, device, s);
+    return pg::launch<TN, 2, 2, pg::SYMMETRIC, pg::MN_MAJOR>(b_s, x_k[cur], P, e, device, s);
   }
   template <int TN, class T, bool KEEP>
   l3_status out(int cur, int done, const Target &t, int64_t rows, int64_t cols) {
@@ -650,7 +641,7 @@ l3_status newton_schulz(const Layout &L, char *ws, int steps, const Target &t, i
   Chain c{L, ws, device, s,
           {reinterpret_cast<__half *>(ws + L.x0), reinterpret_cast<__half *>(ws + L.x1)},
           reinterpret_cast<__half *>(ws + L.a), reinterpret_cast<__half *>(ws + L.b),
-          reinterpret_cast<const int *>(ws + L.exps), L.batch * L.mp, t.fp32, t.fp32 || !t.keep_w};
+          reinterpret_cast<const int *>(ws + L.exps), L.batch * L.mp, t.fp32};
   l3_status st = c.maps();
   const bool wide = L.step.tn == 256;
   for (int i = 0; st == L3_OK && i < steps; ++i) {

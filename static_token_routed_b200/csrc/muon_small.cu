@@ -55,14 +55,14 @@ __device__ __forceinline__ int at(int r, int c) {
   return (c >> 6) * BLOCK + r * 128 + ((((c >> 3) & 7) ^ (r & 7)) << 4) + (c & 7) * 2;
 }
 
-// one thread: D = the products FROM .. 2 of lo hi, hi lo, hi hi over the 16-deep
-// steps k0 .. k1 - 1: A K-major planes at a0 (stride ap), B K-major or MN-major at b0
-template <bool B_MN, int FROM>
+// one thread: D = the products lo hi, hi lo, hi hi over the 16-deep steps k0 .. k1 - 1:
+// A K-major planes at a0 (stride ap), B K-major or MN-major at b0
+template <bool B_MN>
 __device__ __forceinline__ void products(uint32_t d, uint32_t a0, int ap, uint32_t b0, int bp,
                                          int k0, int k1, uint32_t idesc) {
   bool add = false;
 #pragma unroll 1
-  for (int pr = FROM; pr < 3; ++pr) {
+  for (int pr = 0; pr < 3; ++pr) {
     const uint32_t a = a0 + (pr == 0 ? ap : 0), b = b0 + (pr == 1 ? bp : 0);
 #pragma unroll 4
     for (int k = k0; k < k1; ++k) {
@@ -288,7 +288,7 @@ __global__ void __launch_bounds__(THREADS, 1) k_muon_small(const __grid_constant
   const uint32_t tmem = t->tmem_base, s0 = smem_u32(sm);
   const Abort ab{&t->abort_flag, P.err};
   const uint32_t D_A = tmem, D_X = tmem + 256;  // 128 columns each product of A, 256 of X
-  constexpr bool FP32 = sizeof(TO) == 4, FINE = FP32 || !KEEP;  // FINE: A and B in two parts (see muon.cu)
+  constexpr bool FP32 = sizeof(TO) == 4;
   // a warp reads its lane quarter; four warps share a quarter's columns
   const int q = warp & 3, part = warp >> 2, row = q * 32 + lane;
   const uint32_t lane_off = (uint32_t)(q * 32) << 16;
@@ -344,7 +344,7 @@ __global__ void __launch_bounds__(THREADS, 1) k_muon_small(const __grid_constant
   for (int step = 0; step < P.steps; ++step) {
     // A's partial sum over this CTA's columns
     run(ks_x, D_A, D_A + 128, [&](uint32_t d, int k0, int k1) {
-      products<false, 0>(d, s0, X_PLANE, s0, X_PLANE, k0, k1, id_a);
+      products<false>(d, s0, X_PLANE, s0, X_PLANE, k0, k1, id_a);
     });
     float v[32];
     if (square) {
@@ -402,7 +402,7 @@ __global__ void __launch_bounds__(THREADS, 1) k_muon_small(const __grid_constant
       for (int k = 0; k < ROWS / (THREADS / 32); ++k) {
         const int off = OFF_A + at(warp + k * (THREADS / 32), lane * 4);
         *reinterpret_cast<uint2 *>(sm + off) = *reinterpret_cast<uint2 *>(hi[k]);
-        if (FINE) *reinterpret_cast<uint2 *>(sm + A_PLANE + off) = *reinterpret_cast<uint2 *>(lo[k]);
+        *reinterpret_cast<uint2 *>(sm + A_PLANE + off) = *reinterpret_cast<uint2 *>(lo[k]);
       }
     } else if (square) {
       // A in hi + lo, stored as an operand
@@ -415,12 +415,12 @@ __global__ void __launch_bounds__(THREADS, 1) k_muon_small(const __grid_constant
         pack_pair(f, hi, lo);
         const int off = OFF_A + at(row, part * 32 + p * 8);
         *reinterpret_cast<uint4 *>(sm + off) = hi;
-        if (FINE) *reinterpret_cast<uint4 *>(sm + A_PLANE + off) = lo;
+        *reinterpret_cast<uint4 *>(sm + A_PLANE + off) = lo;
       }
     }
     // B = a I + b A + c A A, in A's place once the product has read it
     run(ks_a, D_A + 128, D_A, [&](uint32_t d, int k0, int k1) {
-      products<false, FINE ? 0 : 2>(d, s0 + OFF_A, A_PLANE, s0 + OFF_A, A_PLANE, k0, k1, id_a);
+      products<false>(d, s0 + OFF_A, A_PLANE, s0 + OFF_A, A_PLANE, k0, k1, id_a);
     });
     const float cb = NS_B * exp2f((float)(SB - SA - 2 * e)), cc = NS_C * exp2f((float)(SB - 2 * SA - 4 * e));
     if (square) {
@@ -430,8 +430,7 @@ __global__ void __launch_bounds__(THREADS, 1) k_muon_small(const __grid_constant
       for (int p = 0; p < 4; ++p) {
         const int off = OFF_A + at(row, part * 32 + p * 8);
         float f[8];
-        unpack_pair(*reinterpret_cast<uint4 *>(sm + off),
-                    FINE ? *reinterpret_cast<uint4 *>(sm + A_PLANE + off) : make_uint4(0, 0, 0, 0), f);
+        unpack_pair(*reinterpret_cast<uint4 *>(sm + off), *reinterpret_cast<uint4 *>(sm + A_PLANE + off), f);
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
           f[i] = fmaf(__uint_as_float(u[p * 8 + i]), cc, cb * f[i]);
@@ -440,12 +439,12 @@ __global__ void __launch_bounds__(THREADS, 1) k_muon_small(const __grid_constant
         uint4 hi, lo;
         pack_pair(f, hi, lo);
         *reinterpret_cast<uint4 *>(sm + off) = hi;
-        if (FINE) *reinterpret_cast<uint4 *>(sm + A_PLANE + off) = lo;
+        *reinterpret_cast<uint4 *>(sm + A_PLANE + off) = lo;
       }
     }
     // X' = B X on this CTA's columns
     run(ks_x ? ks_a : 0, D_X, D_A, [&](uint32_t d, int k0, int k1) {
-      products<true, FINE ? 0 : 1>(d, s0 + OFF_A, A_PLANE, s0, X_PLANE, k0, k1, id_x);
+      products<true>(d, s0 + OFF_A, A_PLANE, s0, X_PLANE, k0, k1, id_x);
     });
     const int e_next = max(e - 2, 0);
     const bool last = step + 1 == P.steps;
