@@ -442,7 +442,7 @@ struct EpiGrad {
   static constexpr int BOX_BYTES = 2 * pg::BOX;  // in turn, a plane's 32 columns each
   static constexpr bool LOADS = false;
   static constexpr int WARPS = 8;
-  static constexpr bool SUMS = PLANES > 1;
+  static constexpr bool SUMS = true;
   __device__ __forceinline__ void prefetch(pg::WarpBoxes &, int, int, int) const {}
 
   struct State {
@@ -455,12 +455,26 @@ struct EpiGrad {
                  live ? lse[m] : 0.f, live ? ratio[m] : 0.f};
   }
   __device__ __forceinline__ void chunk(State &s, pg::WarpBoxes &box, int c, float (&v)[32]) const {
+    // a row's target is in few of its columns, and few tiles end inside their columns
+    const bool hit = s.te >= c && s.te < c + 32;
 #pragma unroll
-    for (int e = 0; e < 32; ++e) {
-      float p = ex2((v[e] - s.lse) * LOG2E);
-      if (s.te == c + e) p -= 1.f;
-      v[e] = c + e < s.nv ? p * s.rt : 0.f;
-      if (PLANES < 3 && s.te == c + e && resid) resid[s.m] = v[e] - __bfloat162float(__float2bfloat16_rn(v[e]));
+    for (int e = 0; e < 32; ++e) v[e] = ex2((v[e] - s.lse) * LOG2E);
+    if (hit) {
+#pragma unroll
+      for (int e = 0; e < 32; ++e)
+        if (s.te == c + e) v[e] -= 1.f;
+    }
+#pragma unroll
+    for (int e = 0; e < 32; ++e) v[e] *= s.rt;
+    if (c + 32 > s.nv) {
+#pragma unroll
+      for (int e = 0; e < 32; ++e)
+        if (c + e >= s.nv) v[e] = 0.f;
+    }
+    if (PLANES < 3 && hit && resid) {
+#pragma unroll
+      for (int e = 0; e < 32; ++e)
+        if (s.te == c + e) resid[s.m] = v[e] - __bfloat162float(__float2bfloat16_rn(v[e]));
     }
 #pragma unroll
     for (int p = 0; p < PLANES; ++p) {
@@ -809,11 +823,20 @@ l3_status launch_gather(const GatherParams &G, cudaStream_t s) {
   return L3_OK;
 }
 
+// k-blocks of the logits' chains. The losses are fp32: short chains (bf16 operands
+// 2048 deep in one chain leave the loss 1.7e-6 off; 256-deep ones cost 12 % of the
+// forward pass, 512-deep ones 2 %). Few tokens, whose tiles wait for W, can have
+// shorter ones: a sure token's loss is 2.6e-6 off at worst with 256-deep chains, 1.3e-6
+// with 128-deep ones (64 x 32000 x 1024: 20.8 and 22.8 us; 1 token 20.8 both).
+// The backward pass takes the same chains: in others, a logit drifts away from the
+// lse that holds it, and exp(s - lse) - 1 with it (one chain 4096 deep, logits near
+// 100: 1.5e-3). It costs the gradients of 8192 tokens x 180000 x 2048 2.5 %.
+int logits_chunk(const Layout &L) { return L.fp32 ? 1 : L.n <= 32 ? 2 : L.n <= 128 ? 4 : 8; }
+
 // x W_piece^T with the given epilogue
 template <int PLANES, class Epi>
 l3_status launch_logits(const Layout &L, char *ws, const void *x, const void *W, int64_t v0,
-                        const Epi &epi,
-                        const char *name, int chunk, int device, cudaStream_t s) {
+                        const Epi &epi, const char *name, int device, cudaStream_t s) {
   CUtensorMap mA, mB;
   l3_status st;
   const int64_t rows = std::min(L.vc, L.vocab - v0);
@@ -832,7 +855,7 @@ l3_status launch_logits(const Layout &L, char *ws, const void *x, const void *W,
   P.dyn = L.direct ? nullptr : &head->n_live;
   P.dyn_rows = !L.direct;
   P.clear_err = L.direct;
-  P.chunk = chunk;
+  P.chunk = logits_chunk(L);
   P.group = 16;  // 16 tile rows of x beside a few of W's columns: both stay in L2
   P.bf16 = 1;
   P.b_off = (int)(L.fp32 ? 0 : v0);
@@ -858,10 +881,7 @@ l3_status launch_turned(const Layout &L, Head *head, const void *x, const void *
   P.tiles_m = (int)((L.vocab + 255) / 256);
   P.tiles_n = P.batch = P.group = 1;
   P.nkb = (int)(L.dp / pg::BK);
-  // a sure token's loss is 2.6e-6 off at worst with 256-deep chains, 1.3e-6 with
-  // 128-deep ones, whose additions are in the way of more tokens' (64 x 32000 x
-  // 1024: 20.8 and 22.8 us; 1 token 20.8 both)
-  P.chunk = L.n <= 32 ? 2 : 4;
+  P.chunk = logits_chunk(L);
   P.bf16 = 1;
   P.clear_err = 1;
   P.err = &head->err;
@@ -940,7 +960,7 @@ l3_status backward(const Layout &L, char *ws, const void *x, const void *W, cons
     if ((st = split_w(L, ws, W, v0, device, s)) != L3_OK) return st;
     EpiGrad<GP> eg{{}, G.tgt, G.lse_c, G.ratio, (int)L.np, (int)v0, (int)L.vocab, resid};
     if ((st = pg::box_map(&eg.out, g, true, GP * L.np, L.vc, L.vc)) != L3_OK) return st;
-    if ((st = launch_logits<PLANES>(L, ws, x, W, v0, eg, "xent_grad_logits", FP32 ? 1 : GP == 2 && L.n <= 16 ? 4 : 0, device, s)) != L3_OK) return st;
+    if ((st = launch_logits<PLANES>(L, ws, x, W, v0, eg, "xent_grad_logits", device, s)) != L3_OK) return st;
     // dx += G W: G K-major, W MN-major (its rows are k)
     pg::Problem<pg::K_MAJOR, pg::MN_MAJOR, EpiRows<T>> px{};
     if ((st = pg::operand_map(&px.mA, g, true, GP * L.np, L.vc, L.vc, false, pg::BM)) != L3_OK)
@@ -1086,10 +1106,8 @@ l3_status l3_xent_forward(const void *x, const void *W, const int32_t *targets, 
     for (int64_t i = 0; st == L3_OK && i < L.n_pieces; ++i) {
       es.v0 = (int)(i * L.vc);
       if ((st = split_w(L, ws, W, es.v0, device, s)) != L3_OK) return st;
-      // the losses are fp32: short chains (bf16 operands 2048 deep in one chain
-      // leave the loss 1.7e-6 off; 256-deep ones cost 12 % of the time, 512-deep ones 2 %)
-      st = L.fp32 ? launch_logits<3>(L, ws, x, W, es.v0, es, "xent_logits", 1, device, s)
-                  : launch_logits<1>(L, ws, x, W, es.v0, es, "xent_logits", 8, device, s);
+      st = L.fp32 ? launch_logits<3>(L, ws, x, W, es.v0, es, "xent_logits", device, s)
+                  : launch_logits<1>(L, ws, x, W, es.v0, es, "xent_logits", device, s);
     }
   }
   if (st != L3_OK) return st;
