@@ -296,8 +296,9 @@ l3_status l3_xent_forward(const void *x, const void *W, const int32_t *targets, 
  *   dW     [vocab x d] dtype, out (overwritten; zeros when no token is in);
  *          16-byte aligned
  * G is recomputed in pieces of the vocabulary. For L3_BF16 each element of
- * G / max|g| is rounded to bf16 before the two products, but for the target's
- * in dx and for up to 128 tokens (two parts) in dW. Deterministic.
+ * G / max|g| is rounded to bf16 before the two products, but for the targets'
+ * (16 bits in all). Up to 128 tokens, all elements have 16 bits in dW, and up
+ * to 4 in dx too. Deterministic.
  * Errors as l3_xent_forward.
  */
 l3_status l3_xent_backward(const void *x, const void *W, const int32_t *targets, const float *lse,

@@ -107,6 +107,9 @@ struct Args {
   // and from one matrix of the batch to the next
   int a_off, b_off, a_plane, b_plane, a_batch, b_batch;
   int a_hi;       // of A's two parts (and one of B) only the first
+  // not NULL: the second part only in the k-blocks whose byte [tile row][k-block] is set
+  const uint8_t *a_lo;
+  int a_lo_ld;    // a multiple of 16; rows start 16-byte aligned
   uint32_t bf16;  // 1: bf16 operands, 0: fp16
   int *err;
   int clear_err;  // the chain's first kernel: *err is zeroed (a wait that gives up does so 2 s later)
@@ -341,6 +344,25 @@ struct Order {
   }
 };
 
+// Which k-blocks of a tile row take A's second part; sixteen bytes at a time, from L2
+// (the kernel before wrote them)
+struct SecondPart {
+  const uint4 *row;
+  bool never, always;
+  uint4 w;
+  int have = -1;
+
+  __device__ __forceinline__ SecondPart(const Args &P, int tile_row)
+      : row(reinterpret_cast<const uint4 *>(P.a_lo + (P.a_lo ? (int64_t)tile_row * P.a_lo_ld : 0))),
+        never(P.a_hi), always(!P.a_lo) {}
+  __device__ __forceinline__ bool at(int kb) {
+    if (never || always) return !never;
+    if (kb >> 4 != have) w = __ldcg(row + (have = kb >> 4));
+    const uint32_t x = kb & 8 ? kb & 4 ? w.w : w.z : kb & 4 ? w.y : w.x;
+    return x >> (kb & 3) * 8 & 0xff;
+  }
+};
+
 // An epilogue functor sees a warp's share of a tile, 32 columns at a time:
 //   prefetch(boxes, matrix, row of lane 0, first column c0)   before the tile is done
 //   State begin(matrix, row m, first column c0, dynamic count)
@@ -451,11 +473,13 @@ __global__ void __launch_bounds__(Cfg<TN, typename P1::Epi, typename P2::Epi>::T
         const int m0 = x.mi * (2 * BM) + (int)rank * BM;
         const int n0 = x.ni * TN + (int)rank * (TN / 2);
         const int mat = x.b % sh.matrices;
+        SecondPart second(P, x.mi);
         for (int kb = x.k0; ok && kb < x.k0 + x.k_count; ++kb) {
           const bool a_mn = is_mn(A, kb, x.mi * 256), b_mn = is_mn(B, kb, x.ni * TN);
+          const bool hi = PA > PB && !second.at(kb);
 #pragma unroll
           for (int pl = PL - 1; pl >= 0; --pl) {  // in the order that they are done with
-            if (PA > PB && pl && pb.P.a_hi) continue;
+            if (hi && pl) continue;
             if (!mbar_wait(&b->empty[stage], phase ^ 1, ab)) {
               ok = false;
               break;
@@ -518,6 +542,7 @@ __global__ void __launch_bounds__(Cfg<TN, typename P1::Epi, typename P2::Epi>::T
         constexpr Major A = PT::A, B = PT::B;
         const Tile x = Tile::at<TN>(pb.P, sh, t);
         const int k_count = x.k_count, chunk = PT::Epi::SUMS && pb.P.chunk ? pb.P.chunk : sh.nkb;
+        SecondPart second(pb.P, x.mi);
         for (int i0 = 0; ok && i0 < k_count; i0 += chunk, ++job) {
           const int acc = job % C::ACCS;
           // the epilogue has finished with this accumulator's previous chunk
@@ -529,11 +554,12 @@ __global__ void __launch_bounds__(Cfg<TN, typename P1::Epi, typename P2::Epi>::T
           const uint32_t d = tmem + acc * TN;
           const int i1 = min(k_count, i0 + chunk);
           for (int i = i0; ok && i < i1; ++i) {
+            const bool hi = PA > PB && !second.at(x.k0 + i);
             uint32_t sa[PL];
             uint64_t *empty[PL];  // by part
 #pragma unroll
             for (int pl = PL - 1; pl >= 0; --pl) {
-              if (PA > PB && pl && pb.P.a_hi) continue;
+              if (hi && pl) continue;
               if (!mbar_wait(&b->full[stage], phase, ab)) {
                 ok = false;
                 break;
@@ -553,7 +579,6 @@ __global__ void __launch_bounds__(Cfg<TN, typename P1::Epi, typename P2::Epi>::T
             // rows of 128 bytes down an MN-major one (its 64-wide blocks 8 KB apart)
 #pragma unroll
             for (int pr = 0; pr < Pr::N; ++pr) {
-              const bool hi = PA > PB && pb.P.a_hi;
               if (hi && Pr::a(pr)) continue;
               const uint32_t at = sa[Pr::a(pr)], bt = sa[Pr::b(pr)] + A_BYTES;
 #pragma unroll

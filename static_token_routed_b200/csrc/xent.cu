@@ -23,16 +23,20 @@
 // rows of the others into the workspace, so padding costs nothing and a NaN in
 // it reaches no sum. Their count stays on the device; the products read it.
 //
-// Types. bf16: bf16 operands, fp32 accumulation; G is rounded to bf16 once, the
+// Types. bf16: bf16 operands, fp32 accumulation; G is rounded to bf16, the
 // type of the gradients themselves, without the largest weight max|g|, which
 // multiplies the fp32 accumulators instead: with equal weights, 1 - p near 1 then
 // stays exact. Of the roundings in a row of G the target's alone can weigh as
-// much as all others together, so what it left of that element is kept in fp32 and
-// dx's epilogue adds it times the target's row of W; in dW, tokens average out.
-// Where they are too few for that (n <= 128), dW's G is two bf16 parts, and from
-// 4 tokens or less, where one wrong guess can weigh as much as the target, dx's too.
-// dx is 1.7e-3 off for it, its own rounding, and 2.3e-3 (up to 6e-3
-// from one token) with one part alone. fp32:
+// much as all others together, and so it can in a column, most of whose tokens
+// have other targets. For dx, what it left of that element is kept in fp32 and
+// the epilogue adds it times the target's row of W. For dW, G gets a second bf16 part
+// in the blocks of 64 tokens x 256 columns that hold a target, and the product takes
+// that part in these blocks: at most one a token, and fewer where tokens are frequent
+// (8192 tokens x 180000: 4 % of the blocks). Up to 128 tokens, where one wrong guess can weigh as much as a
+// target, dW takes it everywhere, and dx from 4 tokens or less. dx and dW are 1.7e-3
+// off for it, their own rounding; with one part alone, dx 2.3e-3 (6e-3 from one
+// token) and dW up to 2.4e-3. It costs loss and gradients of 8192 x 180000 x 2048 4 %
+// (19.5 ms) and 1794 live tokens x 32003 x 1024 12 % (519 us). fp32:
 // every operand in three bf16 parts (8 + 8 + 8 bits of the 24), the six
 // products of parts down to 2^-16 of the largest kept.
 #include "attn_common.cuh"
@@ -61,7 +65,9 @@ struct Layout {
   int64_t n, vocab, d;
   bool fp32, bwd;
   int planes;            // bf16 parts of a value of x and W
-  int g_planes, dx_planes;  // and of G, in dW's product and in dx's
+  int g_planes, dx_planes;  // and of G, for dW's product and in dx's
+  bool lo_all;           // G's second part everywhere, or where `lo` says
+  int lo_ld;             // of `lo`: a byte for each 256 columns x 64 tokens of a piece
   int64_t np, dp;        // rows and columns of the gathered x, padded
   int64_t vc, n_pieces;  // vocabulary columns of a piece
   int64_t n_parts;
@@ -72,15 +78,17 @@ struct Layout {
   pg::Tiling logits;
   pg::TwoTilings back;  // dx's and dW's shares
   int part_cols;         // vocabulary columns behind one (max, sum) partial
-  size_t head, idx, tgt, lse, ratio, resid, x, part, tlogit, g, dxacc, dwacc, w, total;
+  size_t head, idx, tgt, lse, ratio, resid, x, part, tlogit, g, lo, dxacc, dwacc, w, total;
 
   Layout(int64_t n_, int64_t vocab_, int64_t d_, bool fp32_, bool bwd_)
       : n(n_), vocab(vocab_), d(d_), fp32(fp32_), bwd(bwd_) {
     planes = fp32 ? 3 : 1;
-    g_planes = fp32 ? 3 : n <= 128 ? 2 : 1;
+    g_planes = fp32 ? 3 : 2;
+    lo_all = fp32 || n <= 128;
     dx_planes = fp32 ? 3 : n <= 4 ? 2 : 1;
     np = round_up(std::max<int64_t>(n, 1), 256);
     dp = round_up(d, 64);
+    lo_ld = (int)round_up(np / 64, 16);
     // a piece's G takes at most 512 MB (one tile column at least), and so do
     // the parts of its rows of an fp32 W: large enough that a piece's products
     // fill the GPU many times over, small beside the memory of the model
@@ -104,7 +112,7 @@ struct Layout {
     part_cols = turned ? 32 : logits.tn / 2;
     n_parts = (vocab + part_cols - 1) / part_cols;
     back = pg::choose_tilings({np / 256, d, vc / pg::BK, np * d, n_pieces > 1, fp32 ? 6 : dx_planes},
-                              {vc / 256, d, np / pg::BK, vc * d, false, fp32 ? 6 : g_planes});
+                              {vc / 256, d, np / pg::BK, vc * d, false, fp32 ? 6 : lo_all ? 2 : 1});
     size_t at = 0;
     auto take = [&](size_t bytes) {
       const size_t r = at;
@@ -121,6 +129,7 @@ struct Layout {
     part = take(bwd ? 0 : (size_t)n_parts * np * 8);
     tlogit = take(bwd ? 0 : np * 4);
     g = take(bwd ? (size_t)g_planes * np * vc * 2 : 0);
+    lo = take(bwd && !lo_all ? (size_t)(vc / 256) * lo_ld : 0);
     dxacc = take(bwd && dx_partial() ? (size_t)back.splits1 * np * d * 4 : 0);
     dwacc = take(bwd && back.splits2 > 1 ? (size_t)back.splits2 * vc * d * 4 : 0);
     w = take(fp32 ? (size_t)planes * vc * dp * 2 : 0);
@@ -438,6 +447,10 @@ struct EpiGrad {
   const float *lse, *ratio;
   int np, v0, vocab;
   float *resid;  // what the target's element lost to the first part, or NULL
+  // not NULL: a byte [256 columns][64 tokens] that says whether the block holds a
+  // target, and the second part only where it does
+  uint8_t *lo;
+  int lo_ld;
 
   static constexpr int BOX_BYTES = 2 * pg::BOX;  // in turn, a plane's 32 columns each
   static constexpr bool LOADS = false;
@@ -448,11 +461,20 @@ struct EpiGrad {
   struct State {
     int nv, te, m, c0;
     float lse, rt;
+    bool parts;  // more than the first
   };
   __device__ __forceinline__ State begin(int, int m, int c0, int n_live) const {
     const bool live = m < n_live;
-    return State{live ? vocab - (v0 + c0) : 0, live ? tgt[m] - (v0 + c0) : -1, m, c0,
-                 live ? lse[m] : 0.f, live ? ratio[m] : 0.f};
+    const int t = live ? tgt[m] - v0 : -1;
+    bool parts = PLANES > 1;
+    if (PLANES == 2 && lo) {
+      // the block's other 32 tokens are another warp's, which comes to the same answer
+      const int t2 = (m ^ 32) < n_live ? tgt[m ^ 32] - v0 : -1, block = c0 >> 8;
+      parts = __any_sync(0xffffffffu, (t >= 0 && t >> 8 == block) || (t2 >= 0 && t2 >> 8 == block));
+      if ((m & 31) == 0) lo[(int64_t)block * lo_ld + (m >> 6)] = parts;
+    }
+    return State{live ? vocab - (v0 + c0) : 0, live ? t - c0 : -1, m, c0,
+                 live ? lse[m] : 0.f, live ? ratio[m] : 0.f, parts};
   }
   __device__ __forceinline__ void chunk(State &s, pg::WarpBoxes &box, int c, float (&v)[32]) const {
     // a row's target is in few of its columns, and few tiles end inside their columns
@@ -478,28 +500,25 @@ struct EpiGrad {
     }
 #pragma unroll
     for (int p = 0; p < PLANES; ++p) {
-      const int b = (c / 32 * PLANES + p) & 1;
+      const int b = (s.parts ? c / 32 * PLANES + p : c / 32) & 1;
       box.stores_read<1>();  // this box's last store
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         uint4 o;
         __nv_bfloat162 *o2 = reinterpret_cast<__nv_bfloat162 *>(&o);
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          float &x = v[j * 8 + 2 * e], &y = v[j * 8 + 2 * e + 1];
-          o2[e] = __floats2bfloat162_rn(x, y);
-          if (p + 1 < PLANES) {  // what the next part has to hold
-            const float2 f = __bfloat1622float2(o2[e]);
-            x -= f.x;
-            y -= f.y;
-          }
-        }
+        for (int e = 0; e < 4; ++e) o2[e] = __floats2bfloat162_rn(v[j * 8 + 2 * e], v[j * 8 + 2 * e + 1]);
         *box.piece(b, j) = o;
       }
       box.written();
       if (box.lane == 0) {
         box.store(b, &out, s.c0 + c, p * np + (s.m & ~31));
         box.commit();
+      }
+      if (!s.parts) break;
+      if (p + 1 < PLANES) {  // what the next part has to hold
+#pragma unroll
+        for (int e = 0; e < 32; ++e) v[e] -= __bfloat162float(__float2bfloat16_rn(v[e]));
       }
     }
   }
@@ -924,13 +943,12 @@ l3_status sum_rows(const SumRows<T> &a, const SumRows<T> &b, const Head *head, i
                          a, b, blocks(a), head, (int)d);
 }
 
-// GP: parts of G
-template <class T, int GP>
+template <class T>
 l3_status backward(const Layout &L, char *ws, const void *x, const void *W, const int32_t *targets,
                    const float *lse, const float *dloss, void *dx, void *dW, int device,
                    cudaStream_t s) {
   constexpr bool FP32 = sizeof(T) == 4;
-  constexpr int PLANES = FP32 ? 3 : 1;
+  constexpr int PLANES = FP32 ? 3 : 1, GP = FP32 ? 3 : 2;  // parts of x and W, and of G
   Head *head = reinterpret_cast<Head *>(ws + L.head);
   GatherParams G = {};
   G.x = x;
@@ -958,7 +976,8 @@ l3_status backward(const Layout &L, char *ws, const void *x, const void *W, cons
     const int64_t v0 = i * L.vc;
     const int64_t rows = std::min(L.vc, L.vocab - v0);
     if ((st = split_w(L, ws, W, v0, device, s)) != L3_OK) return st;
-    EpiGrad<GP> eg{{}, G.tgt, G.lse_c, G.ratio, (int)L.np, (int)v0, (int)L.vocab, resid};
+    uint8_t *lo = L.lo_all ? nullptr : reinterpret_cast<uint8_t *>(ws + L.lo);
+    EpiGrad<GP> eg{{}, G.tgt, G.lse_c, G.ratio, (int)L.np, (int)v0, (int)L.vocab, resid, lo, L.lo_ld};
     if ((st = pg::box_map(&eg.out, g, true, GP * L.np, L.vc, L.vc)) != L3_OK) return st;
     if ((st = launch_logits<PLANES>(L, ws, x, W, v0, eg, "xent_grad_logits", device, s)) != L3_OK) return st;
     // dx += G W: G K-major, W MN-major (its rows are k)
@@ -979,7 +998,7 @@ l3_status backward(const Layout &L, char *ws, const void *x, const void *W, cons
     P.b_off = (int)(FP32 ? 0 : v0);
     P.a_plane = (int)L.np;
     P.b_plane = (int)L.vc;
-    P.a_hi = GP == 2 && L.dx_planes == 1;
+    P.a_hi = L.dx_planes == 1;
     P.err = &head->err;
     px.epi.idx = G.idx;
     px.epi.head = head;
@@ -1003,6 +1022,8 @@ l3_status backward(const Layout &L, char *ws, const void *x, const void *W, cons
       p.P.nkb = (int)(L.np / pg::BK);
       p.P.dyn_rows = 0;
       p.P.a_hi = 0;
+      p.P.a_lo = lo;
+      p.P.a_lo_ld = L.lo_ld;
       p.P.dyn_k = 1;
       p.P.b_off = 0;
       p.P.b_plane = (int)L.np;
@@ -1153,9 +1174,8 @@ l3_status l3_xent_backward(const void *x, const void *W, const int32_t *targets,
     L3_CUDA_TRY(cudaMemsetAsync(dW, 0, (size_t)vocab * d * (L.fp32 ? 4 : 2), s));
     return L3_OK;
   }
-  return L.fp32            ? backward<float, 3>(L, ws, x, W, targets, lse, dloss, dx, dW, device, s)
-         : L.g_planes == 2 ? backward<__nv_bfloat16, 2>(L, ws, x, W, targets, lse, dloss, dx, dW, device, s)
-                           : backward<__nv_bfloat16, 1>(L, ws, x, W, targets, lse, dloss, dx, dW, device, s);
+  return L.fp32 ? backward<float>(L, ws, x, W, targets, lse, dloss, dx, dW, device, s)
+                : backward<__nv_bfloat16>(L, ws, x, W, targets, lse, dloss, dx, dW, device, s);
 }
 
 }  // extern "C"

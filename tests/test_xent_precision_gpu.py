@@ -36,3 +36,36 @@ def test_a_sure_tokens_gradient_is_nothing(n, dtype):
     # dx = G_t W_t, and less than 300 e^-50 of other rows of W
     G = (dx.double() * W.double()[t.long()]).sum(1) / W.double()[t.long()].square().sum(1)
     assert G.abs().max() <= (5e-4 if n <= 128 else 2.0 ** -24)
+
+
+@pytest.mark.parametrize("n,vocab,d,out", [(129, 20000, 512, 0.0), (300, 20000, 512, 0.2), (700, 30011, 272, 0.0),
+                                           (2000, 70000, 272, 0.3)])
+def test_the_targets_element_of_g_is_not_rounded_away_in_dw(n, vocab, d, out):
+    """Most rows of dW have one token whose target they are, and every other element of
+    their G is small: dW is off by its own rounding, not by that of the target's element.
+    By norms: half a step of the other elements times |x|_2; 2^-16 of the targets' (two
+    parts); the logits' errors (chains of 512: 32 steps, each 2^-23 of a sum of magnitudes)
+    and 2^-17 for exponentials; the sums of n terms."""
+    g = torch.Generator().manual_seed(n)
+    W = (0.1 * torch.randn(vocab, d, generator=g) / d ** 0.5).to(BF).cuda()
+    x = torch.randn(n, d, generator=g).to(BF).cuda()
+    t = torch.randint(0, vocab, (n,), generator=g).to(torch.int32)
+    t[torch.rand(n, generator=g) < out] = -1
+    t, w = t.cuda(), ((0.5 + torch.rand(n, generator=g)) / n).cuda()
+    _, lse = l3.l3_xent_forward(x, W, t)
+    _, dW = l3.l3_xent_backward(x, W, t, lse, w)
+    i = (t >= 0).nonzero()[:, 0]
+    X, wd, at = x[i].double(), w[i].double()[:, None], t[i].long()[:, None]
+    s = X @ W.double().T
+    P = (s - torch.logsumexp(s, 1, keepdim=True)).exp() * wd
+    ds = 36 * 2.0 ** -23 * (X.abs() @ W.double().abs().T).amax(1) * 2 + 2.0 ** -17 * (1 + s.abs().amax(1))
+    spectral = torch.linalg.matrix_norm(X, 2)
+    others = (P * (2.0 ** -8 + ds[:, None])).norm() * spectral
+    target = (2.0 ** -16 + ds.max()) * wd.norm() * spectral
+    del s
+    G = P.scatter_add(1, at, -wd)
+    ref = G.T @ X
+    sums = (n + 64) * 2.0 ** -23 * (G.abs().T @ X.abs()).norm()
+    own = (ref.to(BF).double() - ref).norm()
+    assert others + target + sums < 0.3 * own   # what a rounded target's element, 1.3 own, would hide under
+    assert (dW.double() - ref).norm() <= own + others + target + sums
