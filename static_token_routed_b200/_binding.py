@@ -407,13 +407,17 @@ def _output(t, name: str, like: torch.Tensor, shape, dtype, stream):
     return t, _tensor(t, name, dtype, shape, like.device)
 
 
-def _workspace(workspace, n_bytes, like, stream) -> tuple[int, int]:
+def _workspace(workspace, n_bytes, like, stream) -> tuple[torch.Tensor, int, int]:
+    """(tensor, pointer, bytes) of a workspace: the caller's, or a new one. The
+    caller of this holds the tensor until the kernels that use it are enqueued: the
+    call into the library lets other threads run, and freed memory may be handed to
+    one of them."""
     if workspace is None:
-        # freed on return, for what is enqueued later on the stream it was used on
-        return _empty(like, max(n_bytes, 16), torch.uint8, stream).data_ptr(), n_bytes
+        workspace = _empty(like, max(n_bytes, 16), torch.uint8, stream)
+        return workspace, workspace.data_ptr(), n_bytes
     if workspace.device != like.device or not workspace.is_contiguous():
         raise ValueError(f"workspace must be a contiguous tensor on {like.device}")
-    return workspace.data_ptr(), workspace.numel() * workspace.element_size()
+    return workspace, workspace.data_ptr(), workspace.numel() * workspace.element_size()
 
 
 # the current stream's handle without a Stream object around it, where torch has it
@@ -471,7 +475,7 @@ def l3_xent_forward(x: torch.Tensor, W: torch.Tensor, targets: torch.Tensor, los
     pt = _tensor(targets, "targets", torch.int32, (n,), dev)
     loss, pl = _output(loss, "loss", x, (n,), f32, stream)
     lse, pe = _output(lse, "lse", x, (n,), f32, stream)
-    ws = _workspace(workspace, _xent_bytes(n, vocab, d, code, 0), x, stream)
+    held, *ws = _workspace(workspace, _xent_bytes(n, vocab, d, code, 0), x, stream)
     _call(library().l3_xent_forward, dev, px, pw, pt, n, vocab, d, code, pl, pe, *ws,
           _stream_of(stream, dev))
     return loss, lse
@@ -493,7 +497,7 @@ def l3_xent_backward(x: torch.Tensor, W: torch.Tensor, targets: torch.Tensor, ls
     pe, pg = _tensor(lse, "lse", f32, (n,), dev), _tensor(dloss, "dloss", f32, (n,), dev)
     dx, pdx = _output(dx, "dx", x, (n, d), x.dtype, stream)
     dW, pdw = _output(dW, "dW", x, (vocab, d), x.dtype, stream)
-    ws = _workspace(workspace, _xent_bytes(n, vocab, d, code, 1), x, stream)
+    held, *ws = _workspace(workspace, _xent_bytes(n, vocab, d, code, 1), x, stream)
     _call(library().l3_xent_backward, dev, px, pw, pt, pe, pg, n, vocab, d, code, pdx, pdw, *ws,
           _stream_of(stream, dev))
     return dx, dW
@@ -521,7 +525,7 @@ def l3_orthogonalize(G: torch.Tensor, O=None, steps: int = 5, eps: float = 1e-7,
     sizes, dev = _stack(G, "G"), _cuda_device(G, "G")
     pg = _tensor(G, "G", G.dtype, G.shape, dev)
     O, po = _output(O, "O", G, G.shape, G.dtype, stream)  # noqa: E741
-    ws = _workspace(workspace, _muon_bytes(*sizes), G, stream)
+    held, *ws = _workspace(workspace, _muon_bytes(*sizes), G, stream)
     _call(library().l3_orthogonalize, dev, pg, *sizes, code, steps, eps, po, *ws,
           _stream_of(stream, dev))
     return O
@@ -541,7 +545,7 @@ def l3_muon_step(W: torch.Tensor, M: torch.Tensor, G: torch.Tensor, lr: float,
     pg = _tensor(G, "G", torch.float32, W.shape, dev)
     if scale is None:
         scale = max(1.0, sizes[1] / max(1, sizes[2])) ** 0.5
-    ws = _workspace(workspace, _muon_bytes(*sizes), W, stream)
+    held, *ws = _workspace(workspace, _muon_bytes(*sizes), W, stream)
     _call(library().l3_muon_step, dev, pw, pm, pg, *sizes, code, lr, momentum, int(nesterov),
           weight_decay, scale, steps, eps, *ws, _stream_of(stream, dev))
 
