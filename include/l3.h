@@ -247,7 +247,8 @@ l3_status l3_backward(const void *x, l3_plan_t plan, const void *W_K, const void
  * function gives for the same arguments), overwritten by each call, so that a
  * call may be captured into a CUDA graph. Calls that may run at the same time
  * need workspaces of their own, as do graphs that may be replayed at the same
- * time. Work is enqueued on `stream`; nothing synchronizes.
+ * time. Work is enqueued on `stream`; nothing synchronizes. Should a bounded wait
+ * inside a call give up, its outputs (loss and lse; dx and dW; O; W) are NaN.
  */
 
 /* Bytes of workspace for l3_xent_forward (backward = 0) or l3_xent_backward
@@ -354,8 +355,8 @@ l3_status l3_muon_step(void *W, float *M, const float *G, int64_t batch, int64_t
                        int64_t workspace_bytes, void *stream);
 
 /* Synchronizes `stream` and returns L3_ERR_TIMEOUT if a bounded wait inside
- * the call that last used `workspace` gave up (its outputs are then
- * incomplete), L3_ERR_CUDA on a CUDA error, L3_OK otherwise. */
+ * the call that last used `workspace` gave up (its outputs, but for M, are then
+ * NaN), L3_ERR_CUDA on a CUDA error, L3_OK otherwise. */
 l3_status l3_workspace_status(const void *workspace, void *stream);
 
 /*
@@ -463,6 +464,8 @@ l3_status l3_lzw_allocate_device(const int32_t *corpus, int64_t n, int64_t vocab
  * with the kernels' own bounded wait (2 s by %globaltimer). The wait gives
  * up, raises its CTA's abort flag, reports the timeout in device memory and
  * returns; the launch ends normally and the context stays usable.
+ * Also runs, before and after, the launch that turns the results of a chain whose
+ * kernels gave up into NaN (l3_xent_backward, l3_orthogonalize, l3_muon_step).
  * Synchronizes `stream` and takes about 2 s.
  * Returns L3_ERR_TIMEOUT when the give-up was reported (the expected
  * result), L3_ERR_CUDA otherwise.

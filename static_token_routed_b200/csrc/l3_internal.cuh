@@ -205,6 +205,14 @@ l3_status launch_gemm_nt_tc(const void *A, const void *B, const void *A1, const 
                             int64_t M, int64_t N, int64_t K, int64_t lda, int64_t ldb, float *C,
                             int64_t ldc, int *err, int device, cudaStream_t s);
 
+// results of a chain of kernels (16-bit or fp32 elements) and the launch behind it that
+// fills them with NaN if *err is set (give_up.cu); b may be empty
+struct Spoilt {
+  void *p;
+  int64_t bytes;
+};
+l3_status launch_spoil(const int *err, const Spoilt &a, const Spoilt &b, cudaStream_t s);
+
 // GEMMs + LayerNorm, CUDA-core path (gemm_simt.cu)
 l3_status launch_up_ln_simt(const l3_plan_s *p, const void *W_up, const void *gamma,
                             const void *beta, cudaStream_t s);

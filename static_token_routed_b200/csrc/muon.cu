@@ -654,7 +654,9 @@ l3_status newton_schulz(const Layout &L, char *ws, int steps, const Target &t, i
     else
       st = wide ? c.last<256>(cur, i, t, rows, cols) : c.last<128>(cur, i, t, rows, cols);
   }
-  return st;
+  if (st != L3_OK) return st;
+  return launch_spoil(&reinterpret_cast<Head *>(ws + L.head)->err,
+                      {t.out, L.batch * rows * cols * (t.fp32 ? 4 : 2)}, {nullptr, 0}, s);
 }
 
 struct Pointer {

@@ -548,6 +548,12 @@ __global__ void __launch_bounds__(THREADS, 1) k_muon_small(const __grid_constant
   __syncwarp();
   __syncthreads();
   cluster_sync();  // no CTA leaves while another may read its shared memory
+  // a wait that gave up, in this CTA or in another of the cluster: NaN in its columns
+  if (*const_cast<volatile int *>(P.err)) {
+    for (int o = warp; o < outer; o += THREADS / 32)
+      for (int i = lane; i < inner; i += 32)
+        store_el(static_cast<TO *>(P.out) + index(o, i), __int_as_float(0x7fffffff));
+  }
   if (warp == 0) {
     tc_fence_after();
     tmem_dealloc(tmem, 512);

@@ -1057,7 +1057,9 @@ l3_status backward(const Layout &L, char *ws, const void *x, const void *W, cons
       sx = SumRows<T>{px.epi.acc, px.epi.slice, L.back.splits1, G.idx, (int)L.n, static_cast<T *>(dx), lost};
     st = sum_rows(sw, sx, head, L.d, device, s);
   }
-  return st;
+  if (st != L3_OK) return st;
+  const int64_t row = L.d * (int64_t)sizeof(T);
+  return launch_spoil(&head->err, {dx, L.n * row}, {dW, L.vocab * row}, s);
 }
 
 }  // namespace

@@ -1,0 +1,27 @@
+"""What a caller learns when a wait inside the loss's or the update's kernels gives up:
+the error word of its workspace, written here from the host, and results of NaN (the
+launch that writes them is part of l3_check_bounded_wait)."""
+import pytest
+import torch
+
+import static_token_routed_b200 as l3
+
+pytestmark = pytest.mark.gpu
+
+
+def test_status_reads_the_word_of_the_last_call():
+    x = torch.randn(200, 64, device="cuda")
+    ws = torch.empty(l3.l3_muon_workspace(1, 200, 64), dtype=torch.uint8, device="cuda")
+    l3.l3_orthogonalize(x, workspace=ws)
+    l3.l3_workspace_status(ws)
+    ws[:4].view(torch.int32).fill_(4)   # as a give-up leaves it
+    with pytest.raises(l3.L3Error) as e:
+        l3.l3_workspace_status(ws)
+    assert e.value.status == 6
+    l3.l3_orthogonalize(x, workspace=ws)   # a call begins with a clear word
+    l3.l3_workspace_status(ws)
+
+
+def test_results_of_kernels_that_gave_up_are_nan_and_others_are_not_touched():
+    assert l3.l3_check_bounded_wait() == 6, l3.l3_last_error()
+    assert "results" not in l3.l3_last_error()
