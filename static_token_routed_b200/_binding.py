@@ -553,6 +553,8 @@ def l3_muon_step(W: torch.Tensor, M: torch.Tensor, G: torch.Tensor, lr: float,
 def l3_workspace_status(workspace: torch.Tensor, stream=None) -> None:
     """Synchronizes the stream and raises if a bounded device-side wait of the
     call that last used the workspace gave up."""
+    if _cuda_device(workspace, "workspace") and workspace.numel() * workspace.element_size() < 4:
+        raise ValueError("workspace holds no call's error word")
     with torch.cuda.device(workspace.device):
         _check(library().l3_workspace_status(workspace.data_ptr(),
                                              _stream(stream, workspace.device)))

@@ -212,6 +212,11 @@ struct Spoilt {
   int64_t bytes;
 };
 l3_status launch_spoil(const int *err, const Spoilt &a, const Spoilt &b, cudaStream_t s);
+// the error word of a call that has nothing else to do (workspace NULL or short: none)
+inline l3_status clear_error_word(void *workspace, int64_t bytes, cudaStream_t s) {
+  if (workspace && bytes >= 4) L3_CUDA_TRY(cudaMemsetAsync(workspace, 0, 4, s));
+  return L3_OK;
+}
 
 // GEMMs + LayerNorm, CUDA-core path (gemm_simt.cu)
 l3_status launch_up_ln_simt(const l3_plan_s *p, const void *W_up, const void *gamma,

@@ -729,9 +729,10 @@ l3_status l3_orthogonalize(const void *G, int64_t batch, int64_t rows, int64_t c
   const Pointer ptrs[] = {{G, el}, {O, el}, {workspace, 16}};
   l3_status st = check("l3_orthogonalize", batch, rows, cols, dtype, steps, eps, ptrs, 3,
                        workspace_bytes, &device);
-  if (st != L3_OK || batch == 0 || rows == 0 || cols == 0) return st;
-  const Layout L(batch, rows, cols);
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  if (st != L3_OK) return st;
+  if (batch == 0 || rows == 0 || cols == 0) return clear_error_word(workspace, workspace_bytes, s);
+  const Layout L(batch, rows, cols);
   char *ws = static_cast<char *>(workspace);
   UpdateParams U = {};
   U.g = G;
@@ -761,9 +762,10 @@ l3_status l3_muon_step(void *W, float *M, const float *G, int64_t batch, int64_t
   const Pointer ptrs[] = {{W, dtype == L3_FP32 ? 4u : 2u}, {M, 4}, {G, 4}, {workspace, 16}};
   l3_status st = check("l3_muon_step", batch, rows, cols, dtype, steps, eps, ptrs, 4,
                        workspace_bytes, &device);
-  if (st != L3_OK || batch == 0 || rows == 0 || cols == 0) return st;
-  const Layout L(batch, rows, cols);
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  if (st != L3_OK) return st;
+  if (batch == 0 || rows == 0 || cols == 0) return clear_error_word(workspace, workspace_bytes, s);
+  const Layout L(batch, rows, cols);
   char *ws = static_cast<char *>(workspace);
   UpdateParams U = {};
   U.g = G;

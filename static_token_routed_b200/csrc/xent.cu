@@ -1081,9 +1081,10 @@ l3_status l3_xent_forward(const void *x, const void *W, const int32_t *targets, 
   int device = 0;
   const Pointer ptrs[] = {{x, 16}, {W, 16}, {workspace, 16}, {targets, 4}, {loss, 4}, {lse, 4}};
   l3_status st = check(ptrs, 6, n, vocab, d, dtype, workspace_bytes, false, &device);
-  if (st != L3_OK || n == 0) return st;
-  const Layout L(n, vocab, d, dtype == L3_FP32, false);
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  if (st != L3_OK) return st;
+  if (n == 0) return clear_error_word(workspace, workspace_bytes, s);
+  const Layout L(n, vocab, d, dtype == L3_FP32, false);
   char *ws = static_cast<char *>(workspace);
   Head *head = reinterpret_cast<Head *>(ws + L.head);
   JoinParams J = {};
@@ -1174,7 +1175,7 @@ l3_status l3_xent_backward(const void *x, const void *W, const int32_t *targets,
   char *ws = static_cast<char *>(workspace);
   if (n == 0) {
     L3_CUDA_TRY(cudaMemsetAsync(dW, 0, (size_t)vocab * d * (L.fp32 ? 4 : 2), s));
-    return L3_OK;
+    return clear_error_word(workspace, workspace_bytes, s);
   }
   return L.fp32 ? backward<float>(L, ws, x, W, targets, lse, dloss, dx, dW, device, s)
                 : backward<__nv_bfloat16>(L, ws, x, W, targets, lse, dloss, dx, dW, device, s);

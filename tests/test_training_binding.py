@@ -46,3 +46,11 @@ X, W, T, F = torch.ones(4, 16), torch.ones(8, 16), torch.zeros(4, dtype=torch.in
 def test_the_workspace_lives_until_its_kernels_are_enqueued(calls, run):
     run()
     assert len(calls) == 1 and calls[0][1]
+
+
+def test_status_needs_room_for_the_word(monkeypatch):
+    with pytest.raises(ValueError):
+        l3.l3_workspace_status(torch.zeros(16, dtype=torch.uint8))
+    monkeypatch.setattr(b, "_cuda_device", lambda t, name: t.device)
+    with pytest.raises(ValueError):
+        l3.l3_workspace_status(torch.zeros(3, dtype=torch.uint8))
