@@ -327,7 +327,8 @@ int64_t l3_muon_workspace(int64_t batch, int64_t rows, int64_t cols);
  * Products run on pairs of fp16 parts with fp32 accumulation (22 bits): rounding
  * grows with the singular values it meets. Up to 32 rows or columns and 8 steps,
  * they run in 64 bits.
- * Any rows and cols up to 65536, tensors aligned to their elements.
+ * Any rows and cols up to 65536 and batch up to 4096, batch times the smaller of rows
+ * and cols up to 2^27; tensors aligned to their elements.
  * Deterministic. Errors:
  * L3_ERR_INVALID_ARG, L3_ERR_UNSUPPORTED, L3_ERR_CUDA.
  */

@@ -361,10 +361,10 @@ def l3_sort_tokens_noalloc(token_ids: torch.Tensor, vocab: int, perm: torch.Tens
 # ---------------------------------------------------------------------------
 # training around the layer: loss and update
 # ---------------------------------------------------------------------------
-def _dtype_code(t: torch.Tensor, name: str) -> int:
-    if t.dtype == torch.bfloat16:
+def _code(dtype, name: str) -> int:
+    if dtype == torch.bfloat16:
         return L3_BF16
-    if t.dtype == torch.float32:
+    if dtype == torch.float32:
         return L3_FP32
     raise TypeError(f"{name} must be {torch.bfloat16} or {torch.float32}")
 
@@ -454,9 +454,9 @@ def _muon_bytes(batch, rows, cols):
 def l3_xent_workspace(n: int, vocab: int, d: int, dtype=torch.bfloat16,
                       backward: bool = False) -> int:
     """Bytes of workspace of l3_xent_forward, or of l3_xent_backward."""
-    got = _xent_bytes(n, vocab, d, L3_BF16 if dtype == torch.bfloat16 else L3_FP32, int(backward))
+    got = _xent_bytes(n, vocab, d, _code(dtype, "dtype"), int(backward))
     if got < 0:
-        raise L3Error(1, "l3_xent_workspace: sizes out of range")
+        raise L3Error(1, "l3_xent_workspace: sizes that l3_xent_forward and l3_xent_backward reject")
     return got
 
 
@@ -466,7 +466,7 @@ def l3_xent_forward(x: torch.Tensor, W: torch.Tensor, targets: torch.Tensor, los
     log-sum-exp, fp32 [n] each; tokens with a negative target are left out
     (zeros). loss, lse and workspace (l3_xent_workspace bytes) are allocated
     where they are not given."""
-    code = _dtype_code(x, "x")
+    code = _code(x.dtype, "x")
     if x.dim() != 2 or W.dim() != 2:
         raise ValueError("x must be [n, d] and W [vocab, d]")
     (n, d), vocab, dev, f32 = x.shape, W.shape[0], _cuda_device(x, "x"), torch.float32
@@ -487,7 +487,7 @@ def l3_xent_backward(x: torch.Tensor, W: torch.Tensor, targets: torch.Tensor, ls
     """dx [n, d] and dW [vocab, d] of sum_i dloss_i loss_i, in x's type, after
     l3_xent_forward on the same inputs gave lse. dx is l3_backward's dy where x
     is l3_forward's y."""
-    code = _dtype_code(x, "x")
+    code = _code(x.dtype, "x")
     if x.dim() != 2 or W.dim() != 2:
         raise ValueError("x must be [n, d] and W [vocab, d]")
     (n, d), vocab, dev, f32 = x.shape, W.shape[0], _cuda_device(x, "x"), torch.float32
@@ -513,7 +513,7 @@ def l3_muon_workspace(batch: int, rows: int, cols: int) -> int:
     """Bytes of workspace of l3_orthogonalize and l3_muon_step."""
     got = _muon_bytes(batch, rows, cols)
     if got < 0:
-        raise L3Error(1, "l3_muon_workspace: sizes out of range")
+        raise L3Error(1, "l3_muon_workspace: sizes that l3_orthogonalize and l3_muon_step reject")
     return got
 
 
@@ -521,7 +521,7 @@ def l3_orthogonalize(G: torch.Tensor, O=None, steps: int = 5, eps: float = 1e-7,
                      stream=None) -> torch.Tensor:
     """Newton-Schulz orthogonalisation of G [rows, cols], or of each matrix of
     a stack [batch, rows, cols], as Muon does it; O may be G."""
-    code = _dtype_code(G, "G")
+    code = _code(G.dtype, "G")
     sizes, dev = _stack(G, "G"), _cuda_device(G, "G")
     pg = _tensor(G, "G", G.dtype, G.shape, dev)
     O, po = _output(O, "O", G, G.shape, G.dtype, stream)  # noqa: E741
@@ -538,7 +538,7 @@ def l3_muon_step(W: torch.Tensor, M: torch.Tensor, G: torch.Tensor, lr: float,
     """Muon's update of W [rows, cols] (or a stack of such matrices) in place,
     with the fp32 momentum M and gradient G; scale defaults to
     sqrt(max(1, rows / cols))."""
-    code = _dtype_code(W, "W")
+    code = _code(W.dtype, "W")
     sizes, dev = _stack(W, "W"), _cuda_device(W, "W")
     pw = _tensor(W, "W", W.dtype, W.shape, dev)
     pm = _tensor(M, "M", torch.float32, W.shape, dev)

@@ -670,23 +670,34 @@ int vectors(const Pointer *ptrs, int n, int64_t size) {
   return (all & 15) == 0 && size % 8 == 0;
 }
 
+// the sizes that the calls take, before anything is computed from them
+l3_status check_sizes(const std::string &name, int64_t batch, int64_t rows, int64_t cols) {
+  if (batch < 0 || rows < 0 || cols < 0) {
+    set_error(name + ": need batch, rows, cols >= 0");
+    return L3_ERR_INVALID_ARG;
+  }
+  if (rows > 65536 || cols > 65536 || batch > 4096 || 2 * batch * std::min(rows, cols) > (1 << 28)) {
+    set_error(name + ": rows and cols are at most 65536, batch at most 4096, and batch times the "
+                     "smaller of rows and cols at most 2^27");
+    return L3_ERR_UNSUPPORTED;
+  }
+  return L3_OK;
+}
+
 l3_status check(const char *who, int64_t batch, int64_t rows, int64_t cols, int32_t dtype,
                 int32_t steps, float eps, const Pointer *ptrs, int n_ptrs, int64_t ws_bytes,
                 int *device) {
   const std::string name = who;
-  if (batch < 0 || rows < 0 || cols < 0 || (dtype != L3_BF16 && dtype != L3_FP32)) {
-    set_error(name + ": need batch, rows, cols >= 0 and dtype L3_BF16 or L3_FP32");
+  if (dtype != L3_BF16 && dtype != L3_FP32) {
+    set_error(name + ": dtype must be L3_BF16 or L3_FP32");
     return L3_ERR_INVALID_ARG;
   }
   if (steps < 1 || steps > 16 || !(eps >= 0.f)) {
     set_error(name + ": need 1 <= steps <= 16 and eps >= 0");
     return L3_ERR_INVALID_ARG;
   }
-  if (rows > 65536 || cols > 65536 || batch > 4096 || 2 * batch * std::min(rows, cols) > (1 << 28)) {
-    set_error(name + ": rows and cols are at most 65536, batch at most 4096");
-    return L3_ERR_UNSUPPORTED;
-  }
-  if (batch == 0 || rows == 0 || cols == 0) return L3_OK;
+  const l3_status st = check_sizes(name, batch, rows, cols);
+  if (st != L3_OK || batch == 0 || rows == 0 || cols == 0) return st;
   for (int i = 0; i < n_ptrs; ++i) {
     if (!ptrs[i].p) {
       set_error(name + ": a tensor or workspace pointer is NULL");
@@ -715,7 +726,8 @@ using namespace l3;
 extern "C" {
 
 int64_t l3_muon_workspace(int64_t batch, int64_t rows, int64_t cols) {
-  if (batch < 0 || rows < 0 || cols < 0) return -1;
+  set_error("");
+  if (check_sizes("l3_muon_workspace", batch, rows, cols) != L3_OK) return -1;
   if (batch == 0 || rows == 0 || cols == 0) return 0;
   return (int64_t)Layout(batch, rows, cols).total;
 }

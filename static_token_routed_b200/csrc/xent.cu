@@ -800,8 +800,8 @@ struct Pointer {
   uintptr_t align;
 };
 
-l3_status check(const Pointer *ptrs, int n_ptrs, int64_t n, int64_t vocab, int64_t d,
-                int32_t dtype, int64_t ws_bytes, bool bwd, int *device) {
+// the sizes that the calls take, before anything is computed from them
+l3_status check_sizes(int64_t n, int64_t vocab, int64_t d, int32_t dtype) {
   if (n < 0 || vocab < 1 || d < 1 || (dtype != L3_BF16 && dtype != L3_FP32)) {
     set_error("cross entropy: need n >= 0, vocab >= 1, d >= 1 and dtype L3_BF16 or L3_FP32");
     return L3_ERR_INVALID_ARG;
@@ -811,7 +811,13 @@ l3_status check(const Pointer *ptrs, int n_ptrs, int64_t n, int64_t vocab, int64
               "n at most 2^20, vocab at most 2^24");
     return L3_ERR_UNSUPPORTED;
   }
-  if (n == 0 && !bwd) return L3_OK;
+  return L3_OK;
+}
+
+l3_status check(const Pointer *ptrs, int n_ptrs, int64_t n, int64_t vocab, int64_t d,
+                int32_t dtype, int64_t ws_bytes, bool bwd, int *device) {
+  const l3_status st = check_sizes(n, vocab, d, dtype);
+  if (st != L3_OK || (n == 0 && !bwd)) return st;
   for (int i = 0; i < n_ptrs; ++i) {
     if (!ptrs[i].p) {
       set_error("cross entropy: a tensor or workspace pointer is NULL");
@@ -1070,7 +1076,8 @@ using namespace l3;
 extern "C" {
 
 int64_t l3_xent_workspace(int64_t n, int64_t vocab, int64_t d, int32_t dtype, int32_t backward) {
-  if (n < 0 || vocab < 1 || d < 1 || (dtype != L3_BF16 && dtype != L3_FP32)) return -1;
+  set_error("");
+  if (check_sizes(n, vocab, d, dtype) != L3_OK) return -1;
   return (int64_t)Layout(n, vocab, d, dtype == L3_FP32, backward != 0).total;
 }
 
