@@ -68,9 +68,10 @@ struct Layout {
     };
     // a partial is written and read as fp32, half of it (the rest mirrors it)
     gram = pg::choose_tiling(sym_tiles, np / pg::BK, 3, batch * mp * mp / 2);
-    poly = pg::choose_tiling(sym_tiles, mp / pg::BK, 3, batch * mp * mp / 2);
+    // one share: m deep, shares would not be repaid for any m and batch
+    poly = pg::choose_tiling(sym_tiles, mp / pg::BK, 3, INT64_MAX / 1024);
     step = pg::choose_tiling([&](int tn) { return batch * tile_rows * ((np + tn - 1) / tn); }, mp / pg::BK,
-                             3, INT64_MAX / 1024);  // one share
+                             3, INT64_MAX / 1024);
     size_t at = 0;
     auto take = [&](size_t bytes) {
       const size_t r = at;
@@ -84,8 +85,7 @@ struct Layout {
     x1 = take((size_t)2 * batch * mp * np * 2);
     a = take((size_t)2 * batch * mp * mp * 2);
     b = take((size_t)2 * batch * mp * mp * 2);
-    const int shares = std::max(gram.splits, poly.splits);
-    share = take(shares > 1 ? (size_t)shares * batch * mp * mp * 4 : 0);
+    share = take(gram.splits > 1 ? (size_t)gram.splits * batch * mp * mp * 4 : 0);
     total = at;
   }
 };
@@ -312,8 +312,8 @@ struct EpiSym {
   __device__ __forceinline__ void end(State &) const {}
 };
 
-// A share of a symmetric product, fp32, as the accumulator has it; k_sym_join
-// adds the shares up
+// A share of A's product, fp32, as the accumulator has it; k_sym_join adds the
+// shares up
 template <int TN>
 struct EpiShare {
   float *out;  // [share][batch][mp][mp]
@@ -349,20 +349,15 @@ struct EpiShare {
   __device__ __forceinline__ void end(State &) const {}
 };
 
-// The shares of A (POLY = false) or A A (POLY = true) added up in their order,
-// and from the sum A or B as hi + lo planes: a 64 x 64 block in or left of the
-// 256-wide diagonal block per thread block. Memory-bound.
-template <bool POLY>
+// The shares of A added up in their order, and A as hi + lo planes: a 64 x 64
+// block in or left of the 256-wide diagonal block per thread block. Memory-bound.
 __global__ void __launch_bounds__(256) k_sym_join(const float *share, int shares, int64_t batch,
-                                                  int mp, const __half *a, const int *exps,
-                                                  int done, __half *out) {
+                                                  int mp, __half *out) {
   pg::pdl_launch();
   pg::pdl_wait();
   const int bi = blockIdx.y, bj = blockIdx.x, b = blockIdx.z;
   if (bj / 4 > bi / 4) return;
   const int64_t one = (int64_t)mp * mp, plane = batch * one;
-  const int e2 = POLY ? 2 * exp_at(exps, b, done) : 0;
-  const float cb = NS_B * exp2f((float)(SB - SA - e2)), cc = NS_C * exp2f((float)(SB - 2 * SA - 2 * e2));
   const int c = threadIdx.x % 16 * 4;
 #pragma unroll
   for (int k = 0; k < 4; ++k) {
@@ -375,22 +370,10 @@ __global__ void __launch_bounds__(256) k_sym_join(const float *share, int shares
     }
     float f[4] = {s.x, s.y, s.z, s.w};
     __half2 hi[2], lo[2];
-    if (POLY) {
-      *reinterpret_cast<uint2 *>(hi) = *reinterpret_cast<const uint2 *>(a + at);
-      *reinterpret_cast<uint2 *>(lo) = *reinterpret_cast<const uint2 *>(a + plane + at);
-    }
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-      if (POLY) {
-        const float2 x = __half22float2(hi[h]), y = __half22float2(lo[h]);
-        f[2 * h] = fmaf(f[2 * h], cc, cb * (x.x + y.x));
-        f[2 * h + 1] = fmaf(f[2 * h + 1], cc, cb * (x.y + y.y));
-        if (bi == bj && r == c + 2 * h) f[2 * h] += NS_A * exp2f(SB);
-        if (bi == bj && r == c + 2 * h + 1) f[2 * h + 1] += NS_A * exp2f(SB);
-      } else {
-        f[2 * h] *= exp2f(SA - 2 * SX);
-        f[2 * h + 1] *= exp2f(SA - 2 * SX);
-      }
+      f[2 * h] *= exp2f(SA - 2 * SX);
+      f[2 * h + 1] *= exp2f(SA - 2 * SX);
       split2(f[2 * h], f[2 * h + 1], hi[h], lo[h]);
     }
     *reinterpret_cast<uint2 *>(out + at) = *reinterpret_cast<uint2 *>(hi);
@@ -577,19 +560,21 @@ struct Chain {
     P.nkb = (int)((POLY ? L.mp : L.np) / pg::BK);
     EpiSym<TN, POLY> e{POLY ? bm : a, xr * L.mp, {a_box, (int)L.mp, (int)xr}, (int)L.mp, exps, done};
     const CUtensorMap &mA = POLY ? a_s : x_m[cur], &mB = POLY ? a_s : x_n[cur][TN / 256];
-    const int shares = POLY ? L.poly.splits : L.gram.splits;
     LaunchTimer t(POLY ? "muon_poly" : "muon_gram", s);
     constexpr pg::Major MAJOR = POLY ? pg::SYMMETRIC : pg::K_MAJOR;
-    if (shares == 1) return pg::launch<TN, 2, 2, MAJOR, MAJOR>(mA, mB, P, e, device, s);
-    P.splits = shares;
-    P.batch *= shares;
-    const EpiShare<TN> es{reinterpret_cast<float *>(ws + L.share), (int)L.mp};
-    const l3_status st = pg::launch<TN, 2, 2, MAJOR, MAJOR>(mA, mB, P, es, device, s);
-    if (st != L3_OK) return st;
-    const unsigned blocks = (unsigned)(L.mp / 64);
-    return pg::launch_link(k_sym_join<POLY>, dim3(blocks, blocks, (unsigned)L.batch),
-                           dim3(256), s, true, es.out, shares, L.batch, (int)L.mp, a, exps, done,
-                           POLY ? bm : a);
+    if constexpr (!POLY) {
+      if (L.gram.splits > 1) {
+        P.splits = L.gram.splits;
+        P.batch *= P.splits;
+        const EpiShare<TN> es{reinterpret_cast<float *>(ws + L.share), (int)L.mp};
+        const l3_status st = pg::launch<TN, 2, 2, MAJOR, MAJOR>(mA, mB, P, es, device, s);
+        if (st != L3_OK) return st;
+        const unsigned blocks = (unsigned)(L.mp / 64);
+        return pg::launch_link(k_sym_join, dim3(blocks, blocks, (unsigned)L.batch), dim3(256), s, true,
+                               es.out, P.splits, L.batch, (int)L.mp, a);
+      }
+    }
+    return pg::launch<TN, 2, 2, MAJOR, MAJOR>(mA, mB, P, e, device, s);
   }
   template <bool POLY>
   l3_status sym_product(int cur, int done) {
