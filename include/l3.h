@@ -308,7 +308,8 @@ l3_status l3_xent_backward(const void *x, const void *W, const int32_t *targets,
                            void *stream);
 
 /* Bytes of workspace for l3_orthogonalize and l3_muon_step of these sizes; -1
- * for sizes they reject. No device work. */
+ * for sizes they reject. At most about 1 GB, or one matrix's where that is more: larger
+ * stacks go through it in slices. No device work. */
 int64_t l3_muon_workspace(int64_t batch, int64_t rows, int64_t cols);
 
 /*

@@ -41,6 +41,8 @@ struct Head {
   int pad[3];
 };
 
+constexpr int64_t HEAD_BYTES = 1024;
+
 int64_t round_up(int64_t a, int64_t b) { return (a + b - 1) / b * b; }
 
 constexpr int NORM_THREADS = 256;
@@ -78,7 +80,7 @@ struct Layout {
       at += (bytes + 1023) & ~size_t(1023);
       return r;
     };
-    head = take(sizeof(Head));
+    head = take(HEAD_BYTES);
     part = take((size_t)batch * norm_blocks * 8);
     exps = take((size_t)batch * 4);
     x0 = take((size_t)2 * batch * mp * np * 2);
@@ -97,10 +99,10 @@ struct Layout {
 // elements leave fp32's range), one per block; memory-bound
 template <class T, bool MOM>
 __global__ void __launch_bounds__(NORM_THREADS) k_update_norm(UpdateParams P, Head *head,
-                                                              double *part) {
+                                                              bool clear_err, double *part) {
   pg::pdl_launch();
   const int64_t base = (int64_t)blockIdx.y * P.size;
-  if (blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0) head->err = 0;
+  if (clear_err && blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0) head->err = 0;
   double sum = 0.0;
   const int64_t first = blockIdx.x * (int64_t)NORM_THREADS + threadIdx.x;
   const int64_t stride = (int64_t)gridDim.x * NORM_THREADS;
@@ -486,14 +488,14 @@ struct EpiOut {
 };
 
 template <class T, bool MOM>
-l3_status launch_prologue(const Layout &L, const UpdateParams &U, char *ws, float eps,
+l3_status launch_prologue(const Layout &L, const UpdateParams &U, char *ws, float eps, bool clear_err,
                           cudaStream_t s) {
   Head *head = reinterpret_cast<Head *>(ws + L.head);
   double *part = reinterpret_cast<double *>(ws + L.part);
   {
     LaunchTimer t("muon_norm", s);  // the chain's first: waits for all that came before
     k_update_norm<T, MOM><<<dim3((unsigned)L.norm_blocks, (unsigned)L.batch), NORM_THREADS, 0, s>>>(
-        U, head, part);
+        U, head, clear_err, part);
     L3_CUDA_TRY(cudaGetLastError());
   }
   LaunchTimer t("muon_normalise", s);
@@ -621,6 +623,22 @@ struct Chain {
   }
 };
 
+// matrices whose tiles' X, A and B are held at a time: 1 GB of them, one at least.
+// That is far more than fills the GPU, and a stack may be larger than what is free
+// beside it.
+int64_t slice_of(int64_t batch, int64_t rows, int64_t cols) {
+  const int64_t one = (int64_t)Layout(1, rows, cols).total;
+  return std::min(batch, std::max<int64_t>((int64_t(1) << 30) / one, 1));
+}
+
+int64_t workspace_of(int64_t batch, int64_t rows, int64_t cols) {
+  // one launch, whatever the steps and the device: the error word alone
+  if (small_always(std::min(rows, cols), std::max(rows, cols))) return HEAD_BYTES;
+  const int64_t slice = slice_of(batch, rows, cols), rest = batch % slice;
+  // fewer matrices may be shared out more
+  return (int64_t)std::max(Layout(slice, rows, cols).total, rest ? Layout(rest, rows, cols).total : 0);
+}
+
 l3_status newton_schulz(const Layout &L, char *ws, int steps, const Target &t, int64_t rows,
                         int64_t cols, int device, cudaStream_t s) {
   Chain c{L, ws, device, s,
@@ -642,6 +660,28 @@ l3_status newton_schulz(const Layout &L, char *ws, int steps, const Target &t, i
   if (st != L3_OK) return st;
   return launch_spoil(&reinterpret_cast<Head *>(ws + L.head)->err,
                       {t.out, L.batch * rows * cols * (t.fp32 ? 4 : 2)}, {nullptr, 0}, s);
+}
+
+// The whole update, whichever form it takes: U of a gradient of type T (and a momentum)
+// into t
+template <class T, bool MOM>
+l3_status run(UpdateParams U, Target t, int64_t batch, int steps, float eps, char *ws, int device,
+              cudaStream_t s) {
+  const int64_t rows = U.rows, cols = U.cols, m = std::min(rows, cols), n = std::max(rows, cols);
+  int *err = &reinterpret_cast<Head *>(ws)->err;
+  if (tiny_supported(m, steps)) return launch_tiny(U, sizeof(T) == 4, batch, steps, eps, t, err, device, s);
+  if (small_supported(m, n, device)) return launch_small(U, sizeof(T) == 4, batch, steps, eps, t, err, device, s);
+  const int64_t slice = slice_of(batch, rows, cols);
+  for (int64_t b = 0; b < batch; b += slice) {
+    const Layout L(std::min(slice, batch - b), rows, cols);
+    l3_status st = launch_prologue<T, MOM>(L, U, ws, eps, b == 0, s);
+    if (st == L3_OK) st = newton_schulz(L, ws, steps, t, rows, cols, device, s);
+    if (st != L3_OK) return st;
+    U.g = static_cast<const T *>(U.g) + slice * U.size;
+    if (MOM) U.mom += slice * U.size;
+    t.out = static_cast<char *>(t.out) + slice * U.size * (t.fp32 ? 4 : 2);
+  }
+  return L3_OK;
 }
 
 struct Pointer {
@@ -693,10 +733,10 @@ l3_status check(const char *who, int64_t batch, int64_t rows, int64_t cols, int3
       return L3_ERR_INVALID_ARG;
     }
   }
-  const Layout L(batch, rows, cols);
-  if (ws_bytes < (int64_t)L.total) {
+  const int64_t need = workspace_of(batch, rows, cols);
+  if (ws_bytes < need) {
     set_error(name + ": the workspace holds " + std::to_string(ws_bytes) + " bytes, " +
-              std::to_string(L.total) + " are needed");
+              std::to_string(need) + " are needed");
     return L3_ERR_INVALID_ARG;
   }
   L3_CUDA_TRY(cudaGetDevice(device));
@@ -714,7 +754,7 @@ int64_t l3_muon_workspace(int64_t batch, int64_t rows, int64_t cols) {
   set_error("");
   if (check_sizes("l3_muon_workspace", batch, rows, cols) != L3_OK) return -1;
   if (batch == 0 || rows == 0 || cols == 0) return 0;
-  return (int64_t)Layout(batch, rows, cols).total;
+  return workspace_of(batch, rows, cols);
 }
 
 l3_status l3_orthogonalize(const void *G, int64_t batch, int64_t rows, int64_t cols, int32_t dtype,
@@ -729,7 +769,6 @@ l3_status l3_orthogonalize(const void *G, int64_t batch, int64_t rows, int64_t c
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   if (st != L3_OK) return st;
   if (batch == 0 || rows == 0 || cols == 0) return clear_error_word(workspace, workspace_bytes, s);
-  const Layout L(batch, rows, cols);
   char *ws = static_cast<char *>(workspace);
   UpdateParams U = {};
   U.g = G;
@@ -738,16 +777,8 @@ l3_status l3_orthogonalize(const void *G, int64_t batch, int64_t rows, int64_t c
   U.cols = (int)cols;
   U.vec = vectors(ptrs, 2, U.size);
   const Target t{O, dtype == L3_FP32, false, 0.f, 0.f};
-  if (tiny_supported(L.m, steps))
-    return launch_tiny(U, dtype == L3_FP32, batch, steps, eps, t,
-                       &reinterpret_cast<Head *>(ws + L.head)->err, device, s);
-  if (small_supported(L.m, L.n, device))
-    return launch_small(U, dtype == L3_FP32, batch, steps, eps, t,
-                        &reinterpret_cast<Head *>(ws + L.head)->err, device, s);
-  st = dtype == L3_FP32 ? launch_prologue<float, false>(L, U, ws, eps, s)
-                        : launch_prologue<__nv_bfloat16, false>(L, U, ws, eps, s);
-  if (st != L3_OK) return st;
-  return newton_schulz(L, ws, steps, t, rows, cols, device, s);
+  return dtype == L3_FP32 ? run<float, false>(U, t, batch, steps, eps, ws, device, s)
+                          : run<__nv_bfloat16, false>(U, t, batch, steps, eps, ws, device, s);
 }
 
 l3_status l3_muon_step(void *W, float *M, const float *G, int64_t batch, int64_t rows,
@@ -762,7 +793,6 @@ l3_status l3_muon_step(void *W, float *M, const float *G, int64_t batch, int64_t
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   if (st != L3_OK) return st;
   if (batch == 0 || rows == 0 || cols == 0) return clear_error_word(workspace, workspace_bytes, s);
-  const Layout L(batch, rows, cols);
   char *ws = static_cast<char *>(workspace);
   UpdateParams U = {};
   U.g = G;
@@ -774,14 +804,7 @@ l3_status l3_muon_step(void *W, float *M, const float *G, int64_t batch, int64_t
   U.cols = (int)cols;
   U.vec = vectors(ptrs, 3, U.size);
   const Target t{W, dtype == L3_FP32, true, 1.f - lr * weight_decay, lr * scale};
-  if (tiny_supported(L.m, steps))
-    return launch_tiny(U, true, batch, steps, eps, t, &reinterpret_cast<Head *>(ws + L.head)->err, device, s);
-  if (small_supported(L.m, L.n, device))
-    return launch_small(U, true, batch, steps, eps, t,
-                        &reinterpret_cast<Head *>(ws + L.head)->err, device, s);
-  st = launch_prologue<float, true>(L, U, ws, eps, s);
-  if (st != L3_OK) return st;
-  return newton_schulz(L, ws, steps, t, rows, cols, device, s);
+  return run<float, true>(U, t, batch, steps, eps, ws, device, s);
 }
 
 l3_status l3_workspace_status(const void *workspace, void *stream) {

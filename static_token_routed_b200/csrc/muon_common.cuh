@@ -141,6 +141,7 @@ l3_status launch_tiny(const UpdateParams &u, bool g_fp32, int64_t batch, int ste
                       const Target &t, int *err, int device, cudaStream_t s);
 
 // muon_small.cu
+bool small_always(int64_t m, int64_t n);  // on any device
 bool small_supported(int64_t m, int64_t n, int device);
 l3_status launch_small(const UpdateParams &u, bool g_fp32, int64_t batch, int steps, float eps,
                        const Target &t, int *err, int device, cudaStream_t s);

@@ -602,9 +602,10 @@ static bool clusters_of_16(int device) {
   return clusters_fit(k_muon_small<float, false, float, false, false>, MAX_CLUSTER, THREADS, SMEM, known[device & 63]);
 }
 
+bool small_always(int64_t m, int64_t n) { return m <= ROWS && n <= (int64_t)SLAB * 8; }
+
 bool small_supported(int64_t m, int64_t n, int device) {
-  return m <= ROWS && n <= (int64_t)SLAB * MAX_CLUSTER &&
-         (n <= (int64_t)SLAB * 8 || clusters_of_16(device));
+  return small_always(m, n) || (m <= ROWS && n <= (int64_t)SLAB * MAX_CLUSTER && clusters_of_16(device));
 }
 
 l3_status launch_small(const UpdateParams &u, bool g_fp32, int64_t batch, int steps, float eps,

@@ -39,3 +39,28 @@ def test_update_of_a_zero_weight(shape, dtype, kind):
     else:
         own = (X.to(BF).double() - X).norm()
         assert (W.double() + X).norm() <= own + 2 * X_OFF * X.norm()
+
+
+@pytest.mark.parametrize("shape", [(520, 33, 4200), (530, 4100, 5)])
+@pytest.mark.parametrize("dtype", [FP, BF])
+def test_stacks_larger_than_their_workspace(shape, dtype):
+    """Stacks that go through the workspace in slices (5 rows and 9 steps take that way
+    too): every matrix, the last slice's among them, its own results, and nothing
+    outside of the workspace."""
+    steps = 9 if min(shape) == 5 else 5
+    size = l3.l3_muon_workspace(*shape)
+    per_matrix = 8 * 64 * 4160   # X twice, in two fp16 parts, at the least
+    assert size < shape[0] * per_matrix
+    ws = torch.full((size + 4096,), 0xFF, dtype=torch.uint8, device="cuda")
+    G = torch.randn(shape, device="cuda", generator=torch.Generator(device="cuda").manual_seed(5))
+    O = l3.l3_orthogonalize(G.to(dtype), steps=steps, workspace=ws[:size])
+    l3.l3_workspace_status(ws)
+    assert (ws[size:] == 0xFF).all()
+    W, M = torch.zeros(shape, dtype=dtype, device="cuda"), torch.zeros(shape, device="cuda")
+    l3.l3_muon_step(W, M, G, lr=1.0, momentum=0.0, nesterov=False, scale=1.0, steps=steps, workspace=ws[:size])
+    assert (ws[size:] == 0xFF).all() and torch.equal(M, G)
+    for i in list(range(0, shape[0], 37)) + [shape[0] - 1]:
+        for got, of in ((O[i], G[i].to(dtype)), (-W[i], G[i])):
+            X = exact(of, steps)
+            own = (X.to(BF).double() - X).norm() if dtype == BF else 0.0
+            assert (got.double() - X).norm() <= own + 2 * X_OFF * X.norm()

@@ -59,3 +59,13 @@ def test_python_names_the_refusal():
         l3.l3_muon_workspace(1, 65537, 8)
     with pytest.raises(TypeError):
         l3.l3_xent_workspace(8, 100, 64, torch.float16)
+
+
+@pytest.mark.parametrize("batch,rows,cols,most", [
+    (1024, 32, 512, 4096), (4096, 128, 2048, 4096), (4096, 2048, 1, 4096),   # one launch: the error word alone
+    (4096, 1, 65536, 3 << 29), (600, 33, 4200, 3 << 29), (4096, 512, 2048, 3 << 29),
+    (1, 2048, 4096, 120 << 20),
+])
+def test_muon_workspace_is_bounded_in_the_batch(lib, batch, rows, cols, most):
+    assert 0 < lib.l3_muon_workspace(batch, rows, cols) <= most
+    assert 0 < lib.l3_muon_workspace(batch, cols, rows) <= most
