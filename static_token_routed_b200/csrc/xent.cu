@@ -1142,10 +1142,11 @@ l3_status l3_xent_forward(const void *x, const void *W, const int32_t *targets, 
     }
   }
   if (st != L3_OK) return st;
-  // Eight blocks a row group where there are few groups and many partials (one
-  // token, 1000 of them: 20.6 us in all, 24.9 with one block; 256 tokens, 250 of
-  // them: 24.5 and 23.2; 1024 tokens: 57.7 and 55.6)
-  const int cl = n <= 512 && L.n_parts >= 1000 ? 8 : 1;
+  // Eight blocks a row group where there are few groups and many partials. Replayed
+  // back to back (d = 512), eight blocks take longer by, in us: one token, 125 partials
+  // -0.2, 250 -0.9, 500 -2.2, 1000 -4.7; 256 tokens, 125 partials +0.7, 187 -0.3, 500 -1.5; 512 tokens,
+  // 125 partials +0.4, 187 -0.3; 1024 tokens, 500 partials +0.9, 1000 -1.7.
+  const int cl = n <= 512 && L.n_parts >= 160 ? 8 : 1;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)((n + 31) / 32 * cl));
   cfg.blockDim = dim3(32, 32);
