@@ -412,14 +412,13 @@ struct EpiStatsTurned {
   __device__ __forceinline__ void chunk(State &s, pg::WarpBoxes &box, int c, float (&v)[32]) const {
     if (s.c0 + c >= n || (s.m & ~31) >= vocab) return;  // the whole warp alike
     const int tok = s.c0 + c + box.lane;
-    // targets among the warp's rows: few
+    // targets among the warp's rows: in few warps, but there as many as the tokens (a
+    // batch may have the same target throughout)
     const int row = tok < n ? targets[tok] - (s.m & ~31) : -1;
-    for (unsigned hit = __ballot_sync(0xffffffffu, row >= 0 && row < 32); hit; hit &= hit - 1) {
-      const int at = __ffs(hit) - 1;
-      const bool mine = __shfl_sync(0xffffffffu, row, at) == box.lane;
+    if (__any_sync(0xffffffffu, row >= 0 && row < 32)) {
 #pragma unroll
       for (int e = 0; e < 32; ++e)
-        if (mine && e == at) {
+        if (__shfl_sync(0xffffffffu, row, e) == box.lane) {
           tlogit[s.c0 + c + e] = v[e];
           v[e] = -INFINITY;
         }

@@ -69,3 +69,22 @@ def test_the_targets_element_of_g_is_not_rounded_away_in_dw(n, vocab, d, out):
     own = (ref.to(BF).double() - ref).norm()
     assert others + target + sums < 0.3 * own   # what a rounded target's element, 1.3 own, would hide under
     assert (dW.double() - ref).norm() <= own + others + target + sums
+
+
+@pytest.mark.parametrize("n", [2, 32, 60, 128, 200, 600])
+@pytest.mark.parametrize("dtype", [BF, FP])
+@pytest.mark.parametrize("target", [0, 31, 32, 700])
+def test_one_target_for_all_tokens(n, dtype, target):
+    """d = 16 terms, exact for bf16 values and added in one step (2^-23 of a sum of
+    magnitudes below 48); exponentials, their sums and the logarithm 2^-18."""
+    g = torch.Generator(device="cuda").manual_seed(n)
+    x = torch.randn(n, 16, generator=g, device="cuda").to(BF).to(dtype)
+    W = (torch.randn(701, 16, generator=g, device="cuda") / 4).to(BF).to(dtype)
+    t = torch.full((n,), target, dtype=torch.int32, device="cuda")
+    s = x.double() @ W.double().T
+    assert (x.double().abs() @ W.double().abs().T).max() < 48
+    loss, lse = l3.l3_xent_forward(x, W, t)
+    want = torch.logsumexp(s, 1)
+    tol = 48 * 2.0 ** -23 + 2.0 ** -18
+    assert (lse.double() - want).abs().max() <= tol
+    assert (loss.double() - (want - s[:, target])).abs().max() <= 2 * tol
