@@ -171,10 +171,12 @@ struct GatherParams {
 
 constexpr int GATHER_THREADS = 512;
 
-// Each block counts the live tokens before its chunk and in all (every block
-// reads all targets, a few hundred KB from L2 at most), so that one launch
-// orders the rows without atomics. Bound by the copy of x: read once, written
-// once.
+// Each block counts the live tokens before its chunk and in all, so that one launch
+// orders the rows without atomics. Up to some 10^5 tokens the copy of x bounds it, read
+// once and written once (65536 x 1024 bf16: 60 us forward, 113 backward, where the
+// blocks read the weights too). Every block reads all targets, from L2: that
+// grows with the square of n and bounds the largest calls (2^20 x 1024: 1.8 and 4.4 ms,
+// of which the copy is 0.7).
 template <bool FP32, bool BWD>
 __global__ void __launch_bounds__(GATHER_THREADS) k_xent_gather(GatherParams P) {
   pg::pdl_launch();
