@@ -88,3 +88,78 @@ def test_one_target_for_all_tokens(n, dtype, target):
     tol = 48 * 2.0 ** -23 + 2.0 ** -18
     assert (lse.double() - want).abs().max() <= tol
     assert (loss.double() - (want - s[:, target])).abs().max() <= 2 * tol
+
+
+def mantissas(g, shape, bits):
+    """Values in +-[1, 2) with that many random bits in all."""
+    m = torch.randint(1 << (bits - 1), 1 << bits, shape, generator=g, device="cuda")
+    return (m.double() / (1 << (bits - 1))).float() * (torch.randint(0, 2, shape, generator=g, device="cuda") * 2 - 1)
+
+
+@pytest.mark.parametrize("n", [3, 200, 600])
+@pytest.mark.parametrize("x_bits,w_bits", [(24, 1), (1, 24), (12, 12), (16, 8), (8, 16)])
+def test_fp32_logits_keep_all_bits(n, x_bits, w_bits):
+    """One column of W per row, so that each logit is a single product of 24 bits, which
+    the parts of both factors hold exactly: off by 2^-23 of 16 twice at most, as the
+    parts' products have either sign. The exponentials, their sum, the logarithm and the
+    last rounding add 2^-18. Two parts of a factor would leave up to 2^-17 of a logit of 4 to
+    16, 3e-5 to 1.2e-4."""
+    d, vocab = 64, 300
+    g = torch.Generator(device="cuda").manual_seed(n)
+    x = mantissas(g, (n, d), x_bits) * 2
+    W = torch.zeros(vocab, d, device="cuda")
+    j = torch.arange(vocab, device="cuda")
+    W[j, j % d] = mantissas(g, (vocab,), w_bits) * 2
+    t = torch.randint(0, vocab, (n,), generator=g, device="cuda").to(torch.int32)
+    s = x.double() @ W.double().T
+    assert (s.abs() > 0).all() and s.abs().max() < 16
+    loss, lse = l3.l3_xent_forward(x, W, t)
+    want = torch.logsumexp(s, 1)
+    tol = 2 * 2.0 ** -23 * 16 + 2.0 ** -18
+    assert (lse.double() - want).abs().max() <= tol
+    assert (loss.double() - (want - s.gather(1, t.long()[:, None])[:, 0])).abs().max() <= tol
+
+
+@pytest.mark.parametrize("which", ["dx", "dW"])
+def test_fp32_gradients_keep_all_bits_of_g(which):
+    """dW's x, or dx's W, has a single power of two in each column, so that the gradient's
+    elements are G's times it. The probability: s is 2^-23 of 4 off, s - lse, below 14, half
+    a step of 2^-20, its multiple by log2 e, below 21, half a step of 2^-19 (times log 2), the
+    exponential 2^-22 (the reference takes the call's own lse): 2.1e-6 of it in all. The
+    element: p - 1, the weight's ratio, two products by weights and three parts round by 2^-24
+    each, their sum drops 2^-23 twice: 2^-21. Two parts would leave up to 2^-17, 7.6e-6."""
+    g = torch.Generator(device="cuda").manual_seed(1)
+    n, vocab, d = (64, 300, 64) if which == "dW" else (300, 64, 64)
+    eye = torch.eye(64, device="cuda") * 2.0 ** torch.randint(-1, 2, (64, 1), generator=g, device="cuda")
+    full = torch.randn(max(n, vocab), d, generator=g, device="cuda").clamp(-2, 2)
+    x, W = (eye, full) if which == "dW" else (full, eye)
+    t = torch.randint(0, vocab, (n,), generator=g, device="cuda").to(torch.int32)
+    w = 0.5 + torch.rand(n, generator=g, device="cuda")
+    _, lse = l3.l3_xent_forward(x, W, t)
+    dx, dW = l3.l3_xent_backward(x, W, t, lse, w)
+    s = x.double() @ W.double().T
+    assert (s - lse.double()[:, None]).abs().max() < 14
+    p = (s - lse.double()[:, None]).exp()
+    hot = torch.zeros_like(p).scatter_(1, t.long()[:, None], 1.0)
+    G, size = (p - hot) * w.double()[:, None], (p * 2.1e-6 + (p + hot) * 2.0 ** -21) * w.double()[:, None]
+    got, want, tol = (dW, G.T @ x.double(), size.T @ x.double()) if which == "dW" else \
+        (dx, G @ W.double(), size @ W.double())
+    assert ((got.double() - want).abs() <= tol).all()
+
+
+@pytest.mark.parametrize("n", [1, 20, 100, 200, 500])
+def test_bf16_losses_keep_their_chains_short(n):
+    """All terms of one sign, s near 100 from 4096 of them: a chain of 128 (n <= 32), 256
+    (n <= 128) or 512 terms holds 1 / 32, 1 / 16 or 1 / 8 of s < 128, and each of its 8, 16
+    or 32 steps drops up to 2^-23 of the power of two above that: 1.3e-4, 2.5e-4 and 4.9e-4 in
+    all; adding the chains up rounds by 2^-24 of 128 each, 2.5e-4, 1.3e-4 and 6e-5. One
+    chain of 4096 terms was 1.5e-3 off."""
+    d, vocab = 4096, 40
+    g = torch.Generator().manual_seed(n)
+    W = (0.5 + torch.rand(vocab, d, generator=g)).to(BF).cuda()
+    x = ((0.5 + torch.rand(n, d, generator=g)) / 40).to(BF).cuda()
+    t = torch.randint(0, vocab, (n,), generator=g).to(torch.int32).cuda()
+    s = x.double() @ W.double().T
+    assert 90 < s.min() and s.max() < 128
+    _, lse = l3.l3_xent_forward(x, W, t)
+    assert (lse.double() - torch.logsumexp(s, 1)).abs().max() <= 5.5e-4
