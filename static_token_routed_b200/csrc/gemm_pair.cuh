@@ -29,6 +29,11 @@
 // products it enters (2048 x 4096 pairs: 442 instead of 663 MB from L2 in X X^T).
 // The smallest products come first, since the accumulator's own rounding is
 // relative to its size.
+//
+// Times in the comments here and in the files that use this compare the forms of one
+// choice, measured when it was made: calls back to back on the same inputs. Later steps
+// changed the totals: 512 x 512 takes 182 us now, 1000 x 3000 338, 2048 x 4096 864, and 880
+// where the inputs change from call to call.
 #pragma once
 
 #include <algorithm>

@@ -12,7 +12,8 @@
 //
 // The products are the 64-bit matrix instructions (8 x 8 x 4; the tcgen05 ones know
 // no such type): a symmetric product's transposed operand is the same registers as
-// the other one. Bound by latency: 4 x 1000 takes 6.6 us, 16 x 2000 10.8, 32 x 1000
+// the other one. Bound by latency (the kernel alone; a call from Python takes 14 us
+// of host time): 4 x 1000 takes 6.6 us, 16 x 2000 10.8, 32 x 1000
 // 22 (muon_small.cu, with three products of X a step on fewer bits, 72, 78 and
 // 77); a step of 32 rows is 4 products of 16 tiles, 512 instructions at about 11
 // clocks an SM, 3 us (in one chain a tile or in four), and 8 times that at 64.
