@@ -394,7 +394,11 @@ def _empty(like: torch.Tensor, shape, dtype, stream):
     if stream is None:
         return like.new_empty(shape, dtype=dtype)
     if not isinstance(stream, torch.cuda.Stream):
-        stream = torch.cuda.ExternalStream(int(stream), device=like.device)
+        # torch takes a handle of 0 for a request for a stream of its pool, and 1 (the
+        # default stream too) for the ID of one
+        handle = int(stream)
+        stream = (torch.cuda.default_stream(like.device) if handle in (0, 1)
+                  else torch.cuda.ExternalStream(handle, device=like.device))
     with torch.cuda.stream(stream):
         return like.new_empty(shape, dtype=dtype)
 
