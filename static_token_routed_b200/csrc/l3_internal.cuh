@@ -205,6 +205,13 @@ l3_status launch_gemm_nt_tc(const void *A, const void *B, const void *A1, const 
                             int64_t M, int64_t N, int64_t K, int64_t lda, int64_t ldb, float *C,
                             int64_t ldc, int *err, int device, cudaStream_t s);
 
+// The current device, its context current in the calling thread: a thread's first call may
+// encode a tensor map before it launches anything, and that needs one.
+inline cudaError_t current_device(int *device) {
+  const cudaError_t e = cudaGetDevice(device);
+  return e != cudaSuccess ? e : cudaSetDevice(*device);
+}
+
 // results of a chain of kernels (16-bit or fp32 elements) and the launch behind it that
 // fills them with NaN if *err is set (give_up.cu); b may be empty
 struct Spoilt {

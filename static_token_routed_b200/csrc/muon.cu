@@ -739,7 +739,7 @@ l3_status check(const char *who, int64_t batch, int64_t rows, int64_t cols, int3
               std::to_string(need) + " are needed");
     return L3_ERR_INVALID_ARG;
   }
-  L3_CUDA_TRY(cudaGetDevice(device));
+  L3_CUDA_TRY(current_device(device));
   return L3_OK;
 }
 

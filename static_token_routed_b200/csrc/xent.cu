@@ -836,7 +836,7 @@ l3_status check(const Pointer *ptrs, int n_ptrs, int64_t n, int64_t vocab, int64
               std::to_string(L.total) + " are needed");
     return L3_ERR_INVALID_ARG;
   }
-  L3_CUDA_TRY(cudaGetDevice(device));
+  L3_CUDA_TRY(current_device(device));
   return L3_OK;
 }
 
